@@ -83,6 +83,32 @@ class Step(C.Structure):
                 ("topk_idx", p), ("d_status", p), ("out_scales", p)]
 
 
+class Kv4Cache(C.Structure):
+    _fields_ = [("k_codes", p), ("v_codes", p), ("k_scales", p), ("v_scales", p), ("block_table", p),
+                ("num_pages", i32), ("max_blocks", i32), ("kv_heads", i32), ("dim", i32)]
+
+
+class QkNormRopeArgs(C.Structure):
+    _fields_ = [("batch", i32), ("total_tokens", i32), ("q_heads", i32), ("k_heads", i32), ("dim", i32), ("q", p),
+                ("k", p), ("q_stride", C.c_int64), ("k_stride", C.c_int64), ("dtype", C.c_int), ("out_dtype", C.c_int),
+                ("gamma_q", p), ("gamma_k", p), ("eps", C.c_float), ("rope", Rope), ("cu_seqlens", p),
+                ("start_pos", p), ("q_out", p), ("k_out", p), ("d_status", p)]
+
+
+class Kv4AppendArgs(C.Structure):
+    _fields_ = [("batch", i32), ("total_tokens", i32), ("k", p), ("v", p), ("k_stride", C.c_int64),
+                ("v_stride", C.c_int64), ("dtype", C.c_int), ("gamma_k", p), ("eps", C.c_float), ("rope", Rope),
+                ("cu_seqlens", p), ("start_pos", p), ("cache", Kv4Cache), ("q_heads", i32), ("q", p),
+                ("q_stride", C.c_int64), ("gamma_q", p), ("q_out", p), ("q_out_dtype", C.c_int), ("k_stored", p),
+                ("v_stored", p), ("d_status", p)]
+
+
+class Kv4AttentionArgs(C.Structure):
+    _fields_ = [("batch", i32), ("total_tokens", i32), ("max_new", i32), ("heads", i32), ("dim", i32), ("q", p),
+                ("q_stride", C.c_int64), ("cu_seqlens", p), ("start_pos", p), ("cache", Kv4Cache),
+                ("softmax_scale", C.c_float), ("out", p), ("lse", p), ("d_status", p)]
+
+
 EXPORTS = {
     "dsv4_compress": (C.c_int, [C.POINTER(CompressArgs), p]),
     "dsv4_compress_project_workspace_size": (C.c_size_t, [C.POINTER(CompressProjectArgs)]),
@@ -96,6 +122,10 @@ EXPORTS = {
     "dsv4_sparse_mqa_decode": (C.c_int, [C.POINTER(MqaArgs), p, C.c_size_t, p]),
     "dsv4_hybrid_decode_workspace_size": (C.c_size_t, [C.POINTER(Layer), i32]),
     "dsv4_hybrid_decode": (C.c_int, [C.POINTER(Layer), C.POINTER(Step), p, C.c_size_t, p]),
+    "dsv4_qk_norm_rope": (C.c_int, [C.POINTER(QkNormRopeArgs), p]),
+    "dsv4_kv4_append": (C.c_int, [C.POINTER(Kv4AppendArgs), p]),
+    "dsv4_kv4_attention_workspace_size": (C.c_size_t, [C.POINTER(Kv4AttentionArgs)]),
+    "dsv4_kv4_attention": (C.c_int, [C.POINTER(Kv4AttentionArgs), p, C.c_size_t, p]),
     "dsv4_status_string": (C.c_char_p, [C.c_int]),
     "dsv4_abi_version": (i32, []),
     "dsv4_launch_count": (C.c_uint64, []),

@@ -374,6 +374,249 @@ def sparse_mqa_decode(q, pos, cache: DeviceCache, ring: DeviceRing, *, q_dtype: 
     return (res, lse) if with_lse else res
 
 
+# ---------------------------------------------------------------------------
+# the 4-bit key/value cache
+
+KV4_BLOCK = 32  # channels per scale byte
+_ROW_DT = {torch.float32: A.F32, torch.bfloat16: A.BF16}
+
+
+@dataclass
+class DeviceKv4Cache:
+    """Keys and values of one layer in 4 bits: codes [num_pages, kv_heads, 256, dim/2] and scales
+    [num_pages, kv_heads, 256, dim/32], uint8, and the page table [B, max_blocks] int32."""
+    k_codes: torch.Tensor
+    v_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_scales: torch.Tensor
+    block_table: torch.Tensor
+
+    @classmethod
+    def zeros(cls, num_pages: int, kv_heads: int, dim: int, block_table: torch.Tensor) -> "DeviceKv4Cache":
+        def make(n):
+            return torch.zeros((num_pages, kv_heads, A.PAGE_POSITIONS, n), dtype=torch.uint8, device=block_table.device)
+        return cls(make(dim // 2), make(dim // 2), make(dim // KV4_BLOCK), make(dim // KV4_BLOCK), block_table)
+
+    @property
+    def kv_heads(self) -> int:
+        return self.k_codes.shape[1]
+
+    @property
+    def dim(self) -> int:
+        return self.k_codes.shape[3] * 2
+
+    def struct(self) -> A.Kv4Cache:
+        kc, vc, ks, vs, bt = self.k_codes, self.v_codes, self.k_scales, self.v_scales, self.block_table
+        shape = kc.shape
+        if len(shape) != 4 or shape[2] != A.PAGE_POSITIONS or vc.shape != shape:
+            raise ValueError("codes are [num_pages, kv_heads, 256, dim/2], keys like values")
+        if ks.shape != vs.shape or ks.shape[:3] != shape[:3] or ks.shape[3] * KV4_BLOCK != shape[3] * 2:
+            raise ValueError("scales are [num_pages, kv_heads, 256, dim/32], keys like values")
+        for t in (kc, vc, ks, vs):
+            if t.dtype != torch.uint8 or not t.is_contiguous() or t.device != bt.device:
+                raise ValueError("codes and scales are contiguous uint8 tensors on the table's device")
+        if bt.dtype != torch.int32 or bt.dim() != 2 or not bt.is_contiguous():
+            raise ValueError("block_table is a contiguous [B, max_blocks] int32 tensor")
+        return A.Kv4Cache(_ptr(kc), _ptr(vc), _ptr(ks), _ptr(vs), _ptr(bt), shape[0], bt.shape[1], shape[1],
+                          shape[3] * 2)
+
+
+def _rows(name: str, t, heads: int | None = None, dim: int | None = None):
+    """(pointer, elements between tokens) of new tokens' rows [T, heads, dim]; the token axis may be strided."""
+    if t.dim() != 3 or t.dtype not in _ROW_DT:
+        raise ValueError(f"{name} is a [T, heads, dim] float32 or bfloat16 tensor")
+    T, H, D = t.shape
+    if (heads is not None and H != heads) or (dim is not None and D != dim):
+        raise ValueError(f"{name} has {H} heads of {D}, expected {heads} of {dim}")
+    st, sh, sd = t.stride()
+    if sd != 1 or (H > 1 and sh != D):
+        raise ValueError(f"{name}: the heads of a token are contiguous rows")
+    return _ptr(t), (st if T > 1 else H * D)
+
+
+def _lengths(cu_seqlens, start_pos, T_device):
+    if cu_seqlens.dtype != torch.int32 or start_pos.dtype != torch.int32:
+        raise ValueError("cu_seqlens and start_pos are int32 tensors")
+    if cu_seqlens.dim() != 1 or start_pos.dim() != 1 or cu_seqlens.shape[0] != start_pos.shape[0] + 1:
+        raise ValueError("cu_seqlens is [B + 1], start_pos [B]")
+    if not (cu_seqlens.is_contiguous() and start_pos.is_contiguous()):
+        raise ValueError("cu_seqlens and start_pos are contiguous")
+    if cu_seqlens.device != T_device or start_pos.device != T_device:
+        raise ValueError("all tensors of a call are on one device")
+    return start_pos.shape[0]
+
+
+def _dense_out(name, t, shape, dtypes, device):
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} is a contiguous {tuple(shape)} tensor on the inputs' device")
+    return t
+
+
+def _gamma(name, g, dim, device):
+    if g is None:
+        return None
+    if g.dtype != torch.float32 or tuple(g.shape) != (dim,) or not g.is_contiguous() or g.device != device:
+        raise ValueError(f"{name} is a contiguous float32 [{dim}] tensor")
+    return g.data_ptr()
+
+
+def _status_word(d_status, device):
+    if d_status is None:
+        return None
+    if d_status.dtype != torch.int32 or d_status.numel() < 1 or d_status.device != device:
+        raise ValueError("d_status is an int32 tensor on the inputs' device")
+    return d_status.data_ptr()
+
+
+class _On:
+    """The device of a call's tensors made current, and its stream (outputs are allocated there)."""
+
+    def __init__(self, device, stream):
+        self.ctx = []
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(device))
+        if stream is not None:
+            self.ctx.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+
+
+def qk_norm_rope(q, k, cu_seqlens, start_pos, *, gamma_q=None, gamma_k=None, eps: float = 1e-6, rope_dims: int = 64,
+                 rope_base: float = 10000.0, out_dtype=None, q_out=None, k_out=None, d_status=None, stream=None):
+    """RMSNorm of each head of q [T, Hq, D] and k [T, Hk, D] (either may be None), then RoPE of the
+    last rope_dims channels, in one launch. Returns (q_out, k_out), dense, of out_dtype (default:
+    the inputs'). q_out or k_out may be the dense input itself."""
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("qk_norm_rope needs q or k")
+    dev, T, D = some.device, some.shape[0], some.shape[2]
+    if q is not None and k is not None and (k.dtype != q.dtype or k.device != dev or k.shape[0] != T):
+        raise ValueError("q and k have one dtype, device and number of tokens")
+    B = _lengths(cu_seqlens, start_pos, dev)
+    out_dtype = out_dtype or some.dtype
+    with _On(dev, stream) as st:
+        ptrs, outs, heads = [], [], []
+        for name, t, o in (("q", q, q_out), ("k", k, k_out)):
+            if t is None:
+                ptrs.append((None, 0))
+                outs.append(None)
+                heads.append(0)
+                continue
+            ptrs.append(_rows(name, t, dim=D))
+            outs.append(torch.empty(t.shape, dtype=out_dtype, device=dev) if o is None else
+                        _dense_out(name + "_out", o, t.shape, (out_dtype,), dev))
+            heads.append(t.shape[1])
+        a = A.QkNormRopeArgs(B, T, heads[0], heads[1], D, ptrs[0][0], ptrs[1][0], ptrs[0][1], ptrs[1][1],
+                             _ROW_DT[some.dtype], _ROW_DT.get(out_dtype, -1), _gamma("gamma_q", gamma_q, D, dev),
+                             _gamma("gamma_k", gamma_k, D, dev), eps, A.Rope(rope_dims, rope_base),
+                             cu_seqlens.data_ptr(), start_pos.data_ptr(), _ptr(outs[0]), _ptr(outs[1]),
+                             _status_word(d_status, dev))
+        A.check("dsv4_qk_norm_rope", A.load().dsv4_qk_norm_rope(C.byref(a), st))
+    return outs[0], outs[1]
+
+
+def kv4_append(k, v, cu_seqlens, start_pos, cache: DeviceKv4Cache, *, gamma_k=None, eps: float = 1e-6,
+               rope_dims: int = 64, rope_base: float = 10000.0, q=None, gamma_q=None, q_out=None,
+               with_stored: bool = False, k_stored=None, v_stored=None, d_status=None, stream=None):
+    """New tokens' k and v [T, Hk, D] into the 4-bit cache: k normed and rotated, both rounded; q
+    [T, Hq, D], if given, normed and rotated in the same launch (bfloat16, unless q_out says
+    otherwise). Returns (q_out, k_stored, v_stored): None without q; the stored rows' values
+    (bfloat16, exact) with with_stored, else None."""
+    dev, T = k.device, k.shape[0]
+    B = _lengths(cu_seqlens, start_pos, dev)
+    cs = cache.struct()
+    if cache.block_table.shape[0] != B or cache.block_table.device != dev:
+        raise ValueError("the cache's table has one row per sequence, on the inputs' device")
+    if v.dtype != k.dtype or v.device != dev or v.shape != k.shape:
+        raise ValueError("k and v have one shape, dtype and device")
+    if q is not None and (q.dtype != k.dtype or q.device != dev or q.shape[0] != T):
+        raise ValueError("q has k's dtype, device and number of tokens")
+    kp, ks = _rows("k", k, cs.kv_heads, cs.dim)
+    vp, vs = _rows("v", v, cs.kv_heads, cs.dim)
+    with _On(dev, stream) as st:
+        qp, qs, qh, qdt = None, 0, 0, A.BF16
+        if q is not None:
+            qp, qs = _rows("q", q, dim=cs.dim)
+            qh = q.shape[1]
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+            qdt = _ROW_DT[_dense_out("q_out", q_out, q.shape, tuple(_ROW_DT), dev).dtype]
+        elif q_out is not None:
+            raise ValueError("q_out needs q")
+        if with_stored:
+            k_stored = torch.empty(k.shape, dtype=torch.bfloat16, device=dev) if k_stored is None else k_stored
+            v_stored = torch.empty(k.shape, dtype=torch.bfloat16, device=dev) if v_stored is None else v_stored
+        for name, t in (("k_stored", k_stored), ("v_stored", v_stored)):
+            if t is not None:
+                _dense_out(name, t, k.shape, (torch.bfloat16,), dev)
+        a = A.Kv4AppendArgs(B, T, kp, vp, ks, vs, _ROW_DT[k.dtype], _gamma("gamma_k", gamma_k, cs.dim, dev), eps,
+                            A.Rope(rope_dims, rope_base), cu_seqlens.data_ptr(), start_pos.data_ptr(), cs, qh, qp, qs,
+                            _gamma("gamma_q", gamma_q, cs.dim, dev), _ptr(q_out), qdt, _ptr(k_stored), _ptr(v_stored),
+                            _status_word(d_status, dev))
+        A.check("dsv4_kv4_append", A.load().dsv4_kv4_append(C.byref(a), st))
+    return q_out, k_stored, v_stored
+
+
+def kv4_attention_args(q, cu_seqlens, start_pos, cache: DeviceKv4Cache, *, max_new: int, softmax_scale: float = 0.0,
+                       out=None, lse=None, d_status=None) -> A.Kv4AttentionArgs:
+    dev = q.device
+    B = _lengths(cu_seqlens, start_pos, dev)
+    cs = cache.struct()
+    if cache.block_table.shape[0] != B or cache.block_table.device != dev:
+        raise ValueError("the cache's table has one row per sequence, on the inputs' device")
+    if q.dtype != torch.bfloat16:
+        raise ValueError("q is bfloat16")
+    qp, qs = _rows("q", q, dim=cs.dim)
+    if out is not None:
+        _dense_out("out", out, q.shape, (torch.bfloat16,), dev)
+    if lse is not None:
+        _dense_out("lse", lse, q.shape[:2], (torch.float32,), dev)
+    return A.Kv4AttentionArgs(B, q.shape[0], max_new, q.shape[1], cs.dim, qp, qs, cu_seqlens.data_ptr(),
+                              start_pos.data_ptr(), cs, softmax_scale, _ptr(out), _ptr(lse), _status_word(d_status, dev))
+
+
+def kv4_attention_workspace_size(args: A.Kv4AttentionArgs) -> int:
+    """dsv4_kv4_attention_workspace_size for the marshalled arguments of a kv4_attention call."""
+    return A.load().dsv4_kv4_attention_workspace_size(C.byref(args))
+
+
+def kv4_attention_workspace(q, cu_seqlens, cache: DeviceKv4Cache, *, max_new: int) -> torch.Tensor:
+    """A workspace for kv4_attention calls of these sizes (one call at a time may use it)."""
+    with _On(q.device, None):
+        n = kv4_attention_workspace_size(kv4_attention_args(q, cu_seqlens, cu_seqlens[:-1], cache, max_new=max_new))
+        if n == 0:
+            A.check("dsv4_kv4_attention_workspace_size", A.ERR_INVALID_ARG)
+        return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def kv4_attention(q, cu_seqlens, start_pos, cache: DeviceKv4Cache, *, max_new: int, softmax_scale: float = 0.0,
+                  with_lse: bool = False, out=None, lse=None, d_status=None, workspace=None, stream=None):
+    """Causal attention of the new tokens q [T, Hq, D] bfloat16 (normed and rotated) over the 4-bit
+    cache that holds their keys and values already. Returns out, or (out, lse) with with_lse."""
+    dev = q.device
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        if with_lse and lse is None:
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+        a = kv4_attention_args(q, cu_seqlens, start_pos, cache, max_new=max_new, softmax_scale=softmax_scale, out=out,
+                               lse=lse, d_status=d_status)
+        if workspace is None:
+            workspace = torch.empty(max(kv4_attention_workspace_size(a), 256), dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace is a contiguous tensor on the inputs' device")
+        A.check("dsv4_kv4_attention", A.load().dsv4_kv4_attention(
+            C.byref(a), workspace.data_ptr(), workspace.numel() * workspace.element_size(), st))
+    return (out, lse) if with_lse else out
+
+
 def layer_state_bytes(context: int, m: int, entry_width: int, window: int, window_width: int,
                       bytes_per_value: int) -> int:
     return A.load().dsv4_layer_state_bytes(context, m, entry_width, window, window_width, bytes_per_value)

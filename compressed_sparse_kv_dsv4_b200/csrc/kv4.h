@@ -1,0 +1,54 @@
+// Host-side interface of the 4-bit key/value cache kernels (kv4_*.cu), beside internal.h.
+#pragma once
+
+#include "internal.h"
+
+namespace dsv4 {
+
+constexpr int kKv4Block = 32;               // channels that share one power-of-two scale
+constexpr int kKv4ExpMin = -23;             // scale exponents: every code times its scale is then
+constexpr int kKv4ExpMax = 13;              // an exact fp16 (and bf16) value
+
+struct Kv4Cache {
+  uint8_t *k_codes, *v_codes;    // [num_pages][Hk][256][D / 2]
+  uint8_t *k_scales, *v_scales;  // [num_pages][Hk][256][D / 32]
+  const int32_t *block_table;    // [B][max_blocks]
+  int num_pages, max_blocks;
+};
+
+// Head norms and rotation of new tokens (cache.k_codes null: q and k to q_out and k_out;
+// otherwise q to q_out, k and v to the cache).
+struct Kv4HeadsLaunch {
+  int B, T, Hq, Hk, D;
+  const void *q, *k, *v;                  // rows of D values, heads contiguous
+  int64_t q_stride, k_stride, v_stride;   // elements between tokens
+  dsv4_dtype in_dt, out_dt;               // F32 or BF16
+  const float *gamma_q, *gamma_k;         // [D], null: no norm
+  float eps;
+  int rope_dims;
+  float rope_base;
+  double rope_theta1 = 1.0;               // filled by the launcher
+  const int32_t *cu_seqlens, *start_pos;
+  void *q_out, *k_out;                    // [T][H][D]
+  uint16_t *k_stored, *v_stored;          // [T][Hk][D] bf16, optional (cache only)
+  Kv4Cache cache;
+  uint32_t *d_status;
+};
+cudaError_t launch_kv4_heads(const Kv4HeadsLaunch &p, cudaStream_t st);
+
+struct Kv4AttnLaunch {
+  int B, T, Hq, Hk, D;
+  int max_new;              // the most new tokens of a sequence (chooses the kernel, nothing else)
+  const uint16_t *q;        // [T][Hq][D] bf16
+  int64_t q_stride;         // elements between tokens
+  const int32_t *cu_seqlens, *start_pos;
+  Kv4Cache cache;
+  float softmax_scale;      // > 0
+  uint16_t *out;            // [T][Hq][D] bf16
+  float *lse;               // [T][Hq] or null
+  uint32_t *d_status;
+};
+size_t kv4_attention_workspace_bytes(const Kv4AttnLaunch &p);
+cudaError_t launch_kv4_attention(const Kv4AttnLaunch &p, void *ws, cudaStream_t st);
+
+}  // namespace dsv4

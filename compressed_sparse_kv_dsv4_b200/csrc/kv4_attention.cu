@@ -1,0 +1,704 @@
+// Attention over the 4-bit key/value cache, rows in small tiles: decode steps, draft tokens.
+//
+// Query token i of sequence s sits at position p = start + i and sees positions 0..p:
+//   o = sum_j softmax_j( scale * q . k_j ) v_j,   lse = ln sum_j exp( scale * q . k_j )
+// The rows that share a key/value head's keys are the G = Hq / Hk query heads of each new token;
+// a unit of work is a row tile of R = 8 NT of them, of one key/value head of one sequence.
+//
+// Bound by memory when the rows are few: each cached value is 4.25 bits and is used once per
+// row tile. So all units' keys, in tiles of 64, form one line that is cut into equal slices,
+// one per CTA, whatever the sequences' lengths: every CTA reads the same number of bytes, and a
+// long sequence is split over many CTAs. A unit that one CTA has whole is written directly; the
+// parts of the others go through the workspace and kv4_combine_kernel joins them (a fixed
+// order, so results do not depend on timing).
+//
+// Inside a CTA a producer lane brings each tile of 64 keys into a ring of shared-memory stages
+// with four bulk copies (codes and scales of a head's rows are contiguous within a page), and
+// each of four warps takes every fourth tile whole: the products, an online softmax of its own and
+// the weighted sum of values, in registers; the warps' sums are joined at the end of the slice's
+// part of the unit. The matrix products are mma.sync m16n8k16 (fp16 operands, fp32 sums) with
+// keys (S^T = K Q^T) and channels (O^T = V^T P^T) on the 16-row side and rows on the 8-column
+// side: a decode step has G rows, far fewer than a tcgen05 tile's 128, and the operand is made in
+// registers from 4-bit codes, where mma.sync takes it without a trip through shared memory.
+//  - Codes become fp16 pairs with the hardware's e2m1x2 conversion; a product with the block's
+//    power of two is exact (|value| <= 49152, a multiple of 2^-24).
+//  - q (bf16) is scaled by a power of two per row into fp16's range, which is exact but for
+//    elements 2^-39 below the row's largest.
+//  - P is rounded to fp16 (relative 2^-11 / 2, of weights scaled by 2^14); its sum is fp32 of the
+//    unrounded weights, so lse carries no rounding of P.
+// The channel order of the products is free: a lane takes 16 consecutive bytes of a key's codes
+// (K) and D/16 of a value's (V), and Q's fragments and the output's addresses follow that order.
+// A value block with scale 255 (NaN) counts as zero in the product; the smallest such position is
+// noted per block of channels and rows that see it become NaN at the end, so that a row for which
+// the position is masked is not touched by it.
+#include "common.cuh"
+#include "kv4.h"
+
+namespace dsv4 {
+
+namespace {
+
+constexpr int kTile = 64;       // keys of a stage
+constexpr int kWarps = 4;       // consumer warps
+constexpr int kThreadsA = 32 * (kWarps + 1);
+constexpr float kPOff = 14.f;   // weights are held times 2^14
+constexpr int kMinTiles = 4;    // tiles of a slice, at least (one per warp)
+
+struct AttnParams {
+  Kv4AttnLaunch a;
+  float *part_o;     // [2 slots][R][D] per CTA: unnormalised sums
+  float2 *part_ml;   // [2 slots][R] per CTA: maximum (log2) and sum
+  int ctas;
+};
+
+// ---------------------------------------------------------------- the line of work
+
+// new tokens and positions of sequence s; false (and d_status) where they make no sense
+struct Seq {
+  int tok0, len, start, n;  // first token, new tokens, first position, positions to read
+};
+__device__ __forceinline__ bool seq_info(const Kv4AttnLaunch &p, int s, Seq *q, bool tell) {
+  const int64_t c0 = p.cu_seqlens[s], c1 = p.cu_seqlens[s + 1], st = p.start_pos[s];
+  const int64_t cap = static_cast<int64_t>(p.cache.max_blocks) * DSV4_PAGE_POSITIONS;
+  if (c0 < 0 || c1 < c0 || c1 > p.T || st < 0) {
+    if (tell) report(p.d_status, DSV4_DEV_BAD_LENGTH);
+    return false;
+  }
+  if (c1 == c0) return false;
+  int64_t n = st + (c1 - c0);
+  if (n > cap) {
+    if (tell) report(p.d_status, DSV4_DEV_BAD_LENGTH);
+    n = cap;
+  }
+  q->tok0 = static_cast<int>(c0);
+  q->len = static_cast<int>(c1 - c0);
+  q->start = static_cast<int>(st < cap ? st : cap);  // (a row behind the capacity sees what there is)
+  q->n = static_cast<int>(n);
+  return true;
+}
+
+struct Line {
+  const Kv4AttnLaunch *p;
+  int G, R;
+  __device__ __forceinline__ int row_tiles(const Seq &q) const {
+    return static_cast<int>((static_cast<int64_t>(q.len) * G + R - 1) / R);
+  }
+  __device__ __forceinline__ int tiles(const Seq &q) const { return (q.n + kTile - 1) / kTile; }
+  __device__ __forceinline__ int64_t weight(int s, bool tell = false) const {
+    Seq q;
+    if (!seq_info(*p, s, &q, tell)) return 0;
+    return static_cast<int64_t>(p->Hk) * row_tiles(q) * tiles(q);
+  }
+};
+
+// prefix[i]: tiles of the sequences before i * chunk; prefix[n]: all. Called by all `n` threads of
+// the block (n a multiple of 32, up to 1024).
+__device__ __forceinline__ int64_t line_prefix(const Line &ln, int n, int chunk, int64_t *prefix, int64_t *warp_sums) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t mine = 0;
+  for (int i = 0; i < chunk; ++i) {
+    const int64_t s = static_cast<int64_t>(tid) * chunk + i;
+    if (s < ln.p->B) mine += ln.weight(static_cast<int>(s), blockIdx.x == 0);
+  }
+  int64_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += up;
+  }
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  int64_t base = 0, all = 0;
+  for (int w = 0; w < n / 32; ++w) {
+    if (w < warp) base += warp_sums[w];
+    all += warp_sums[w];
+  }
+  prefix[tid] = base + inc - mine;
+  if (tid == n - 1) prefix[n] = all;
+  __syncthreads();
+  return all;
+}
+
+// Walks the units of [at, end) of the line. Every role of a CTA walks the same one.
+struct Walk {
+  Line ln;
+  int64_t at, end;
+  int s, row_tiles, tiles, kvh, rt;  // the unit that `at` lies in
+  int tile;                          // and the tile in it
+  Seq q;
+
+  __device__ __forceinline__ void begin(const Line &line, const int64_t *prefix, int n, int chunk, int64_t from,
+                                        int64_t to) {
+    ln = line;
+    at = from;
+    end = to;
+    int lo = 0, hi = n;  // the last thread's chunk that starts at or before `from`
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (prefix[mid] <= from) lo = mid;
+      else hi = mid;
+    }
+    int64_t base = prefix[lo];
+    s = lo * chunk;
+    for (;; ++s) {
+      const int64_t w = ln.weight(s);
+      if (base + w > from) break;
+      base += w;
+    }
+    load(from - base);
+  }
+  __device__ __forceinline__ void load(int64_t off) {
+    seq_info(*ln.p, s, &q, false);
+    row_tiles = ln.row_tiles(q);
+    tiles = ln.tiles(q);
+    const int64_t unit = off / tiles;
+    tile = static_cast<int>(off % tiles);
+    kvh = static_cast<int>(unit / row_tiles);
+    rt = static_cast<int>(unit % row_tiles);
+  }
+  // the part of the current unit that lies in the slice: tiles [tile, stop)
+  __device__ __forceinline__ int stop() const {
+    const int64_t left = end - at;
+    return left < tiles - tile ? tile + static_cast<int>(left) : tiles;
+  }
+  __device__ __forceinline__ bool next() {  // false: the slice is done
+    at += stop() - tile;
+    if (at >= end) return false;
+    tile = 0;
+    if (++rt == row_tiles) {
+      rt = 0;
+      if (++kvh == ln.p->Hk) {
+        kvh = 0;
+        do ++s;
+        while (ln.weight(s) == 0);
+        load(0);
+      }
+    }
+    return true;
+  }
+  // positions that any row of the unit sees
+  __device__ __forceinline__ int unit_limit() const {
+    const int64_t last = min(static_cast<int64_t>(q.len) * ln.G, static_cast<int64_t>(rt + 1) * ln.R) - 1;
+    return min(q.n, q.start + static_cast<int>(last / ln.G) + 1);
+  }
+  // positions that row r of the unit sees (0: there is no such row)
+  __device__ __forceinline__ int row_limit(int r) const {
+    const int64_t row = static_cast<int64_t>(rt) * ln.R + r;
+    if (row >= static_cast<int64_t>(q.len) * ln.G) return 0;
+    return min(q.n, q.start + static_cast<int>(row / ln.G) + 1);
+  }
+  // [token][head] index of row r
+  __device__ __forceinline__ int64_t row_index(int r) const {
+    const int64_t row = static_cast<int64_t>(rt) * ln.R + r;
+    return (q.tok0 + row / ln.G) * ln.p->Hq + kvh * ln.G + row % ln.G;
+  }
+};
+
+__device__ __forceinline__ int64_t slice_at(int64_t all, int ctas, int c) {
+  // (all is at most 2^31 tokens' row tiles times 2^25 tiles; the quotient form stays in 64 bits)
+  return all / ctas * c + all % ctas * c / ctas;
+}
+__device__ __forceinline__ int slices(int64_t all, int ctas) {
+  const int64_t most = (all + kMinTiles - 1) / kMinTiles;
+  return most < ctas ? static_cast<int>(most) : ctas;
+}
+
+// ---------------------------------------------------------------- fragments
+
+// a byte of two e2m1 codes -> fp16 pair; four bytes at once
+__device__ __forceinline__ void e2m1x8_to_half2(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// scale byte -> 2^(byte - 127) as float (255: NaN)
+__device__ __forceinline__ float scale_value(uint32_t b) {
+  return __uint_as_float(b << 23 | (b == 255u ? 0x400000u : 0u));
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+// Row of a 16-key group that fragment row g (0..7) stands for: neighbouring pairs differ in parity
+// (a quarter warp's 16-byte reads of two 64-byte rows touch all banks), and so do the even ones
+// (the four rows of a value read meet two to a bank, not four).
+__device__ __forceinline__ int key_of(int g) { return (g & 4) + ((0x2130 >> (4 * (g & 3))) & 3); }
+
+template <int D, int NT>
+struct StageBytes {
+  static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / kKv4Block;
+  static constexpr int kStage = 2 * (kCodes + kScales);
+  static constexpr int kStages = D == 128 ? (NT == 1 ? 6 : 8) : 8;
+};
+
+template <int D, int NT>
+struct alignas(128) AttnSmem {
+  using SB = StageBytes<D, NT>;
+  struct alignas(128) Stage {
+    uint8_t k[SB::kCodes], v[SB::kCodes], ks[SB::kScales], vs[SB::kScales];
+  } stage[SB::kStages];
+  float o[kWarps][8 * NT][D + 4];  // the warps' sums, joined at the end of a unit's part
+  float2 ml[kWarps][8 * NT];
+  int64_t prefix[kThreadsA + 1], warp_sums[kThreadsA / 32];
+  uint64_t full[SB::kStages], empty[SB::kStages];
+  int bad[SB::kStages];            // the stage's page does not exist
+  int nan_at[D / kKv4Block];       // smallest position with a NaN value block
+  int abort_flag;
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreadsA, NT == 1 ? 3 : 2) kv4_step_kernel(const __grid_constant__ AttnParams P) {
+  constexpr int R = 8 * NT, KS = D / 16, MT = kTile / 16;
+  using SB = StageBytes<D, NT>;
+  constexpr int NS = SB::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  using Smem = AttnSmem<D, NT>;
+  Smem &S = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  const Kv4AttnLaunch &p = P.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&S.full[i], 1);
+      mbar_init(&S.empty[i], 1);
+    }
+    S.abort_flag = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  const Line line{&p, p.Hq / p.Hk, R};
+  const int chunk = (p.B + kThreadsA - 1) / kThreadsA;
+  const int64_t all = line_prefix(line, kThreadsA, chunk, S.prefix, S.warp_sums);
+  const int ctas = slices(all, P.ctas);
+  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  const int64_t from = slice_at(all, ctas, blockIdx.x), to = slice_at(all, ctas, blockIdx.x + 1);
+  Walk w;
+  w.begin(line, S.prefix, kThreadsA, chunk, from, to);
+
+  if (warp == kWarps) {
+    // ---------------- producer
+    if (lane == 0) {
+      fence_proxy_async_global();  // the cache's rows may come from the kernel before, by plain stores
+      int issued = 0;
+      bool ok = true;
+      do {
+        const int stop = min(w.stop(), (w.unit_limit() + kTile - 1) / kTile);
+        const int32_t *table = p.cache.block_table + static_cast<int64_t>(w.s) * p.cache.max_blocks;
+        for (int t = w.tile; ok && t < stop; ++t) {
+          const int slot = issued % NS;
+          const int page = table[t / (DSV4_PAGE_POSITIONS / kTile)];
+          if (issued >= NS && !mbar_wait(&S.empty[slot], (issued / NS - 1) & 1, &S.abort_flag)) {
+            ok = false;
+            break;
+          }
+          const bool bad = page < 0 || page >= p.cache.num_pages;
+          S.bad[slot] = bad;
+          if (bad) {
+            report(p.d_status, DSV4_DEV_BAD_PAGE);
+            mbar_arrive(&S.full[slot]);
+          } else {
+            const int64_t row = (static_cast<int64_t>(page) * p.Hk + w.kvh) * DSV4_PAGE_POSITIONS +
+                                t % (DSV4_PAGE_POSITIONS / kTile) * kTile;
+            mbar_arrive_expect_tx(&S.full[slot], SB::kStage);
+            bulk_load(S.stage[slot].k, p.cache.k_codes + row * (D / 2), SB::kCodes, &S.full[slot]);
+            bulk_load(S.stage[slot].ks, p.cache.k_scales + row * (D / kKv4Block), SB::kScales, &S.full[slot]);
+            bulk_load(S.stage[slot].v, p.cache.v_codes + row * (D / 2), SB::kCodes, &S.full[slot]);
+            bulk_load(S.stage[slot].vs, p.cache.v_scales + row * (D / kKv4Block), SB::kScales, &S.full[slot]);
+          }
+          ++issued;
+        }
+      } while (w.next() && ok);
+      if (!ok || *static_cast<volatile int *>(&S.abort_flag)) {  // let the copies in flight land before the CTA leaves
+        for (int n = issued > NS ? NS : issued; n >= 1; --n) {
+          const int i = issued - n;
+          volatile int dummy = 0;
+          mbar_wait(&S.full[i % NS], (i / NS) & 1, &dummy);
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------- consumers
+    const int g = lane >> 2, t4 = lane & 3;
+    int done = 0;     // stages of the CTA before the current unit's part
+    bool dead = false;
+    do {
+      const int stop = w.stop(), limit = w.unit_limit();
+      const int vis = min(stop, (limit + kTile - 1) / kTile);
+      // Q fragments: column g of tile nt is row 8 nt + g; a lane's channels of step j are D/4 t4 + 4 j ..+3
+      uint32_t qf[NT][KS][2];
+      float rs[NT][2];   // log2 score per product, of columns 2 t4 and 2 t4 + 1
+      int lim[NT][2];
+      int least = limit; // positions that every row sees
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = 8 * nt + g, rl = w.row_limit(r);
+        uint32_t raw[KS * 2];
+        uint32_t am = 0;
+        if (rl > 0) {
+          const int64_t row = static_cast<int64_t>(w.rt) * R + r;
+          const uint16_t *src = p.q + (w.q.tok0 + row / line.G) * p.q_stride +
+                                static_cast<int64_t>(w.kvh * line.G + row % line.G) * D + t4 * (D / 4);
+#pragma unroll
+          for (int i = 0; i < KS / 2; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(src + 8 * i);
+            raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
+          }
+#pragma unroll
+          for (int i = 0; i < KS * 2; ++i) am = max(am, max((raw[i] << 16) & 0x7FFF0000u, raw[i] & 0x7FFF0000u));
+        } else {
+#pragma unroll
+          for (int i = 0; i < KS * 2; ++i) raw[i] = 0;
+        }
+        am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+        am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+        // 2^sh brings the largest element to [2^14, 2^15) (bounded so that 2^sh and 2^-sh are normal)
+        const int ex = static_cast<int>(am >> 23) - 127;
+        const int sh = (am == 0 || ex >= 128) ? 0 : min(max(14 - ex, -113), 120);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+#pragma unroll
+        for (int i = 0; i < KS * 2; ++i) {
+          const float lo = __uint_as_float(raw[i] << 16) * up, hi = __uint_as_float(raw[i] & 0xFFFF0000u) * up;
+          qf[nt][i >> 1][i & 1] = pack_half2(lo, hi);
+        }
+        const float mine = p.softmax_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+        rs[nt][0] = __shfl_sync(0xFFFFFFFFu, mine, 8 * t4);      // lane 4 * (2 t4): column 2 t4
+        rs[nt][1] = __shfl_sync(0xFFFFFFFFu, mine, 8 * t4 + 4);
+        lim[nt][0] = w.row_limit(8 * nt + 2 * t4);
+        lim[nt][1] = w.row_limit(8 * nt + 2 * t4 + 1);
+        least = min(least, min(lim[nt][0], lim[nt][1]));
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
+      if (tid < D / kKv4Block) S.nan_at[tid] = 0x7FFFFFFF;
+      named_bar_sync(1, 32 * kWarps);
+
+      float o[KS][NT][4];
+      float m[NT][2], l[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+      }
+      const int count = max(vis - w.tile, 0);
+      // stage i of the CTA goes to warp i % 4
+      for (int i = (warp - done % kWarps + kWarps) % kWarps; i < count; i += kWarps) {
+        const int st = done + i, slot = st % NS;
+        if (dead) break;
+        const bool ok = mbar_wait(&S.full[slot], (st / NS) & 1, &S.abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          dead = true;
+          break;
+        }
+        const typename Smem::Stage &T = S.stage[slot];
+        if (S.bad[slot]) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.empty[slot]);
+          continue;
+        }
+        const int key0 = (w.tile + i) * kTile;
+        const bool edge = key0 + kTile > least;
+        float s[MT][NT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const int ra = 16 * mt + key_of(g), rb = ra + 8;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
+          constexpr int W = D / 32;  // words of a lane's codes of one key
+          uint32_t ca[W], cb[W];
+          if constexpr (W == 4) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(T.k + ra * (D / 2) + t4 * 16);
+            const uint4 b = *reinterpret_cast<const uint4 *>(T.k + rb * (D / 2) + t4 * 16);
+            ca[0] = a.x, ca[1] = a.y, ca[2] = a.z, ca[3] = a.w;
+            cb[0] = b.x, cb[1] = b.y, cb[2] = b.z, cb[3] = b.w;
+          } else {
+            const uint2 a = *reinterpret_cast<const uint2 *>(T.k + ra * (D / 2) + t4 * 8);
+            const uint2 b = *reinterpret_cast<const uint2 *>(T.k + rb * (D / 2) + t4 * 8);
+            ca[0] = a.x, ca[1] = a.y;
+            cb[0] = b.x, cb[1] = b.y;
+          }
+          const int blk = t4 * (D / 4) / kKv4Block;
+          const float fa = scale_value(T.ks[ra * (D / kKv4Block) + blk]), fb = scale_value(T.ks[rb * (D / kKv4Block) + blk]);
+          const uint32_t sa = pack_half2(fa, fa), sb = pack_half2(fb, fb);
+#pragma unroll
+          for (int c = 0; c < W; ++c) {
+            uint32_t ha[4], hb[4];
+            e2m1x8_to_half2(ca[c], ha);
+            e2m1x8_to_half2(cb[c], hb);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t a0 = hmul2(ha[2 * k], sa), a2 = hmul2(ha[2 * k + 1], sa);
+              const uint32_t a1 = hmul2(hb[2 * k], sb), a3 = hmul2(hb[2 * k + 1], sb);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816(s[mt][nt], a0, a1, a2, a3, qf[nt][2 * c + k][0], qf[nt][2 * c + k][1]);
+            }
+          }
+        }
+        // softmax: column c of tile nt is this lane's row pair; keys g and g + 8 of each 16
+        if (edge) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const int ka = key0 + 16 * mt + key_of(g);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                if (ka >= lim[nt][c]) s[mt][nt][c] = -INFINITY;
+                if (ka + 8 >= lim[nt][c]) s[mt][nt][2 + c] = -INFINITY;
+              }
+            }
+          }
+        }
+        uint32_t pb[MT][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float off[2];
+          bool moved = false;
+          float keep[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float x = s[0][nt][c];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) x = fmaxf(x, fmaxf(s[mt][nt][c], s[mt][nt][2 + c]));
+#pragma unroll
+            for (int o2 = 4; o2 < 32; o2 <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o2));
+            const float now = fmaxf(m[nt][c], x * rs[nt][c]);
+            keep[c] = now == -INFINITY ? 1.f : ex2_approx(m[nt][c] - now);
+            moved |= now != m[nt][c];
+            m[nt][c] = now;
+            off[c] = now == -INFINITY ? 0.f : kPOff - now;
+          }
+          if (__any_sync(0xFFFFFFFFu, moved)) {
+            l[nt][0] *= keep[0];
+            l[nt][1] *= keep[1];
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              o[k][nt][0] *= keep[0], o[k][nt][1] *= keep[1];
+              o[k][nt][2] *= keep[0], o[k][nt][3] *= keep[1];
+            }
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const float p0 = ex2_approx(fmaf(s[mt][nt][0], rs[nt][0], off[0]));
+            const float p1 = ex2_approx(fmaf(s[mt][nt][1], rs[nt][1], off[1]));
+            const float p2 = ex2_approx(fmaf(s[mt][nt][2], rs[nt][0], off[0]));
+            const float p3 = ex2_approx(fmaf(s[mt][nt][3], rs[nt][1], off[1]));
+            l[nt][0] += p0 + p2;
+            l[nt][1] += p1 + p3;
+            pb[mt][nt][0] = transpose8(pack_half2(p0, p1));
+            pb[mt][nt][1] = transpose8(pack_half2(p2, p3));
+          }
+        }
+        // O^T += V^T P^T: a lane's channels are D/8 g .. + D/8 - 1, its keys 2 t4, 2 t4 + 1 and those + 8
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const int kA = 16 * mt + key_of(2 * t4), kB = 16 * mt + key_of(2 * t4 + 1);
+          constexpr int W = D / 64;
+          uint32_t c4[4][W];
+          uint32_t sb[4];
+          const int blk = g * (D / 8) / kKv4Block;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int key = ((q & 1) ? kB : kA) + (q >> 1) * 8;
+            const uint8_t *src = T.v + key * (D / 2) + g * (D / 16);
+            if constexpr (W == 2) {
+              const uint2 v = *reinterpret_cast<const uint2 *>(src);
+              c4[q][0] = v.x, c4[q][1] = v.y;
+            } else {
+              c4[q][0] = *reinterpret_cast<const uint32_t *>(src);
+            }
+            sb[q] = T.vs[key * (D / kKv4Block) + blk];
+            if (edge && key0 + key >= limit) sb[q] = 0;  // not a position of the unit: 2^-127, zero in fp16
+          }
+          if (max(max(sb[0], sb[1]), max(sb[2], sb[3])) == 255u) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (sb[q] == 255u) {
+                atomicMin(&S.nan_at[blk], key0 + ((q & 1) ? kB : kA) + (q >> 1) * 8);
+                sb[q] = 0;
+              }
+          }
+          const uint32_t sAB = pack_half2(scale_value(sb[0]), scale_value(sb[1]));
+          const uint32_t sCD = pack_half2(scale_value(sb[2]), scale_value(sb[3]));
+#pragma unroll
+          for (int c = 0; c < W; ++c) {
+            uint32_t h[4][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) e2m1x8_to_half2(c4[q][c], h[q]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t a0 = hmul2(__byte_perm(h[0][k], h[1][k], 0x5410), sAB);
+              const uint32_t a1 = hmul2(__byte_perm(h[0][k], h[1][k], 0x7632), sAB);
+              const uint32_t a2 = hmul2(__byte_perm(h[2][k], h[3][k], 0x5410), sCD);
+              const uint32_t a3 = hmul2(__byte_perm(h[2][k], h[3][k], 0x7632), sCD);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816(o[4 * c + k][nt], a0, a1, a2, a3, pb[mt][nt][0], pb[mt][nt][1]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.empty[slot]);
+      }
+      done += count;
+
+      // ---- join the warps
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float x = l[nt][c];
+#pragma unroll
+          for (int o2 = 4; o2 < 32; o2 <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o2);
+          const int r = 8 * nt + 2 * t4 + c;
+          if (g == 0) S.ml[warp][r] = make_float2(m[nt][c], x);
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            const int d = g * (D / 8) + 2 * k;
+            *reinterpret_cast<float2 *>(&S.o[warp][r][d]) = make_float2(o[k][nt][c], o[k][nt][2 + c]);
+          }
+        }
+      }
+      named_bar_sync(1, 32 * kWarps);
+      const bool whole = w.tile == 0 && stop == w.tiles;
+      const int slot = 2 * static_cast<int>(blockIdx.x) + (w.tile == 0 ? 1 : 0);
+      constexpr int V4 = D / 4;
+      for (int e = tid; e < R * V4; e += 32 * kWarps) {
+        const int r = e / V4, d = e % V4 * 4;
+        const int rl = w.row_limit(r);
+        if (rl == 0) continue;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) mx = fmaxf(mx, S.ml[k][r].x);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+          const float2 ml = S.ml[k][r];
+          const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2_approx(ml.x - mx);
+          const float4 v = *reinterpret_cast<const float4 *>(&S.o[k][r][d]);
+          sum = fmaf(ml.y, f, sum);
+          acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
+          acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
+        }
+        if (S.nan_at[d / kKv4Block] < rl) acc.x = acc.y = acc.z = acc.w = __uint_as_float(0x7FC00000u);
+        if (whole) {
+          const int64_t row = w.row_index(r);
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          const uint2 b = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          *reinterpret_cast<uint2 *>(p.out + row * D + d) = b;
+          if (d == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (mx - kPOff + log2f(sum)) * 0.6931471805599453f;
+        } else {
+          *reinterpret_cast<float4 *>(P.part_o + (static_cast<int64_t>(slot) * R + r) * D + d) = acc;
+          if (d == 0) P.part_ml[slot * R + r] = make_float2(mx, sum);
+        }
+      }
+      named_bar_sync(1, 32 * kWarps);
+    } while (w.next());
+  }
+  if (S.abort_flag && lane == 0) report(p.d_status, DSV4_DEV_TIMEOUT);
+}
+
+// Joins the parts of a unit that several slices share: CTA c takes the unit that slice c starts
+// inside of, if no earlier slice does.
+constexpr int kCombineThreads = 128;
+template <int D>
+__global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const __grid_constant__ AttnParams P, int R) {
+  __shared__ int64_t prefix[kCombineThreads + 1], warp_sums[kCombineThreads / 32];
+  const Kv4AttnLaunch &p = P.a;
+  pdl_wait();
+  pdl_launch_dependents();
+  const Line line{&p, p.Hq / p.Hk, R};
+  const int chunk = (p.B + kCombineThreads - 1) / kCombineThreads;
+  const int64_t all = line_prefix(line, kCombineThreads, chunk, prefix, warp_sums);
+  const int ctas = slices(all, P.ctas);
+  const int c = static_cast<int>(blockIdx.x) + 1;
+  if (c >= ctas) return;
+  Walk w;
+  const int64_t from = slice_at(all, ctas, c);
+  w.begin(line, prefix, kCombineThreads, chunk, from, from + 1);
+  const int64_t unit = from - w.tile;
+  if (w.tile == 0 || slice_at(all, ctas, c - 1) > unit) return;
+  int last = c;
+  while (last + 1 < ctas && slice_at(all, ctas, last + 1) < unit + w.tiles) ++last;
+  constexpr int V4 = D / 4;
+  for (int e = threadIdx.x; e < R * V4; e += kCombineThreads) {
+    const int r = e / V4, d = e % V4 * 4;
+    if (w.row_limit(r) == 0) continue;
+    float mx = -INFINITY;
+    for (int k = c - 1; k <= last; ++k) mx = fmaxf(mx, P.part_ml[(2 * k + (k == c - 1)) * R + r].x);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    for (int k = c - 1; k <= last; ++k) {
+      const int64_t slot = 2 * k + (k == c - 1);
+      const float2 ml = P.part_ml[slot * R + r];
+      const float4 v = *reinterpret_cast<const float4 *>(P.part_o + (slot * R + r) * D + d);
+      const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2_approx(ml.x - mx);
+      sum = fmaf(ml.y, f, sum);
+      acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
+      acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
+    }
+    const int64_t row = w.row_index(r);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2 *>(p.out + row * D + d) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (d == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (mx - kPOff + log2f(sum)) * 0.6931471805599453f;
+  }
+}
+
+// rows of a tile: one tile of 8 where the rows of a sequence fit, two otherwise
+int tile_rows(const Kv4AttnLaunch &p) { return static_cast<int64_t>(p.max_new) * (p.Hq / p.Hk) <= 8 ? 8 : 16; }
+int resident(int R) { return R == 8 ? 3 : 2; }
+
+template <int D, int NT>
+cudaError_t launch_step(AttnParams &P, cudaStream_t st) {
+  const size_t smem = sizeof(AttnSmem<D, NT>) + 128;
+  cudaError_t e = cudaFuncSetAttribute(kv4_step_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kv4_step_kernel<D, NT>, dim3(P.ctas), dim3(kThreadsA), smem, st, 1, P);
+  if (e != cudaSuccess || P.ctas == 1) return e;
+  return launch_pdl(kv4_combine_kernel<D>, dim3(P.ctas - 1), dim3(kCombineThreads), 0, st, 1, P, 8 * NT);
+}
+
+}  // namespace
+
+size_t kv4_attention_workspace_bytes(const Kv4AttnLaunch &p) {
+  const int R = tile_rows(p);
+  const size_t rows = static_cast<size_t>(sm_count()) * resident(R) * 2 * R;
+  return align_up(rows * p.D * sizeof(float), 256) + align_up(rows * sizeof(float2), 256);
+}
+
+cudaError_t launch_kv4_attention(const Kv4AttnLaunch &q, void *ws, cudaStream_t st) {
+  AttnParams P{};
+  P.a = q;
+  const int R = tile_rows(q);
+  P.ctas = sm_count() * resident(R);
+  P.part_o = static_cast<float *>(ws);
+  P.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(ws) +
+                                         align_up(static_cast<size_t>(P.ctas) * 2 * R * q.D * sizeof(float), 256));
+  if (q.D == 64) return R == 8 ? launch_step<64, 1>(P, st) : launch_step<64, 2>(P, st);
+  return R == 8 ? launch_step<128, 1>(P, st) : launch_step<128, 2>(P, st);
+}
+
+}  // namespace dsv4

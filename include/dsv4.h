@@ -417,6 +417,150 @@ dsv4_status dsv4_hybrid_decode(const dsv4_layer *layer, const dsv4_step *step, v
                                size_t workspace_bytes, dsv4_stream stream);
 
 /* ------------------------------------------------------------------------------------
+ * The 4-bit key/value cache: ordinary grouped-query attention layers beside the hybrid ones,
+ * with separate keys and values for each key/value head, held in 4 bits.
+ *
+ * Position t of sequence s is row t % 256 of page block_table[s*max_blocks + t/256]. A page holds
+ * for each key/value head 256 rows: k_codes and v_codes [num_pages][kv_heads][256][dim/2] (OCP
+ * e2m1 codes, two per byte, the even channel in the low nibble) and k_scales and v_scales
+ * [num_pages][kv_heads][256][dim/32], one byte per 32 channels (value = code * 2^(byte - 127);
+ * 255: the block reads as NaN). Exponents lie in [-23, 13], so every stored value is exact in
+ * fp16 and in bf16; other bytes (below 104, 141 to 254) are not allowed. 4.25 bits per value.
+ * All four arrays are 16-byte aligned. max_blocks <= 2^22.
+ *
+ * The calls below share the layout of new tokens: sequence s brings tokens cu_seqlens[s] ..
+ * cu_seqlens[s+1]-1 (device int32 [batch+1], from 0, not decreasing) at positions start_pos[s],
+ * start_pos[s]+1, ... (device int32 [batch], >= 0). A sequence may bring none. Output rows of
+ * tokens at or behind cu_seqlens[batch] are left as they are. Rows of a token's heads are
+ * contiguous; tokens are `stride` elements apart (0: heads * dim; otherwise at least that and a
+ * multiple of 16 bytes). Row pointers are 16-byte aligned. total_tokens <= 2^26, head counts <=
+ * 2^14, batch <= 65535.
+ */
+typedef struct {
+  void *k_codes, *v_codes;
+  void *k_scales, *v_scales;
+  const int32_t *block_table; /* [batch][max_blocks] */
+  int32_t num_pages;
+  int32_t max_blocks;
+  int32_t kv_heads;
+  int32_t dim;
+} dsv4_kv4_cache;
+
+/*
+ * dsv4_qk_norm_rope: RMSNorm of each query and key head, then RoPE, in one pass (vLLM "Q-norm +
+ * KV RoPE"), for layers whose keys go elsewhere than to the 4-bit cache:
+ *   out = RoPE_p( x / sqrt(mean(x^2) + eps) * gamma )
+ * A NULL gamma leaves that norm out; q_heads or k_heads may be 0 (the pointers are then ignored).
+ * dim 64, 128, 256 or 512. dtype (of q and k) and out_dtype: F32 or BF16; each output is rounded
+ * once. q_out [total_tokens][q_heads][dim] and k_out are dense; an output may be its own input
+ * if that is dense too and has the same dtype. No workspace.
+ */
+typedef struct {
+  int32_t batch;
+  int32_t total_tokens;
+  int32_t q_heads;
+  int32_t k_heads;
+  int32_t dim;
+  const void *q;
+  const void *k;
+  int64_t q_stride;
+  int64_t k_stride;
+  dsv4_dtype dtype;
+  dsv4_dtype out_dtype;
+  const float *gamma_q; /* [dim] or NULL */
+  const float *gamma_k; /* [dim] or NULL */
+  float eps;
+  dsv4_rope rope;
+  const int32_t *cu_seqlens;
+  const int32_t *start_pos;
+  void *q_out;
+  void *k_out;
+  uint32_t *d_status;
+} dsv4_qk_norm_rope_args;
+
+dsv4_status dsv4_qk_norm_rope(const dsv4_qk_norm_rope_args *args, dsv4_stream stream);
+
+/*
+ * dsv4_kv4_append: new tokens into the 4-bit cache (vLLM "Q-norm + KV RoPE + K insert"). Keys are
+ * normed with gamma_k (NULL: not) and rotated as above, values taken as they are; both are
+ * rounded in blocks of 32 channels and written at their positions. A block's scale is the smallest
+ * power of two 2^k with amax <= 6 * 2^k, -23 <= k <= 13 (2^0 for a zero block); the codes are
+ * the nearest, ties to even, saturating. A block with an infinity or a NaN is stored as NaN.
+ *   k, v  [total_tokens][cache.kv_heads][cache.dim] in dtype (F32 or BF16), cache.dim 64 or 128
+ *   q     optional (q_heads > 0): the same tokens' queries, normed with gamma_q and rotated in
+ *         the same pass into q_out [total_tokens][q_heads][dim] (q_out_dtype F32 or BF16)
+ *   k_stored, v_stored  optional [total_tokens][kv_heads][dim] bf16: the rows as the cache now
+ *         holds them (exact), for a prompt's attention outside the cache, or to see what was rounded
+ * A token whose position has no page (beyond max_blocks, or a page id out of range) is not
+ * written and reported; its q_out row is. Two tokens of one call must not share a cache row.
+ * No workspace.
+ */
+typedef struct {
+  int32_t batch;
+  int32_t total_tokens;
+  const void *k;
+  const void *v;
+  int64_t k_stride;
+  int64_t v_stride;
+  dsv4_dtype dtype;     /* of k, v and q */
+  const float *gamma_k; /* [dim] or NULL */
+  float eps;
+  dsv4_rope rope;
+  const int32_t *cu_seqlens;
+  const int32_t *start_pos;
+  dsv4_kv4_cache cache;
+  int32_t q_heads;
+  const void *q;
+  int64_t q_stride;
+  const float *gamma_q; /* [dim] or NULL */
+  void *q_out;
+  dsv4_dtype q_out_dtype;
+  void *k_stored;
+  void *v_stored;
+  uint32_t *d_status;
+} dsv4_kv4_append_args;
+
+dsv4_status dsv4_kv4_append(const dsv4_kv4_append_args *args, dsv4_stream stream);
+
+/*
+ * dsv4_kv4_attention: causal attention of the new tokens over the 4-bit cache, which holds them
+ * already (append first). Token i of sequence s, at position p = start_pos[s] + i, attends
+ * positions 0..p; head h reads key/value head h / (heads / kv_heads):
+ *   out = sum_j softmax_j( softmax_scale * q . k_j ) * v_j,  lse = ln sum_j exp(softmax_scale * q . k_j)
+ * One token per sequence (a decode step), a few (draft tokens) or a whole prompt, mixed freely.
+ *   q, out [total_tokens][heads][dim] bf16 (q strided, out dense), dim 64 or 128, q as
+ *   dsv4_kv4_append leaves it; lse [total_tokens][heads] float32 or NULL; softmax_scale <= 0
+ *   means 1/sqrt(dim).
+ *   max_new: the most new tokens that a sequence of the batch brings. It chooses the kernel;
+ *   results are right for any value >= 1.
+ * Positions on a page with an id out of range are left out and reported; positions beyond the
+ * table's capacity do not exist (reported). A row that is left with no position gets a zero output
+ * and lse -inf. A NaN in a key or value makes NaN of the rows that see it and of no other.
+ * Workspace: dsv4_kv4_attention_workspace_size() bytes (of the sizes alone: q, out and lse may be
+ * NULL there), 256-byte aligned; what it holds does not matter before the call or after it.
+ */
+typedef struct {
+  int32_t batch;
+  int32_t total_tokens;
+  int32_t max_new;
+  int32_t heads;
+  int32_t dim;
+  const void *q;
+  int64_t q_stride;
+  const int32_t *cu_seqlens;
+  const int32_t *start_pos;
+  dsv4_kv4_cache cache;
+  float softmax_scale;
+  void *out;
+  float *lse;
+  uint32_t *d_status;
+} dsv4_kv4_attention_args;
+
+size_t dsv4_kv4_attention_workspace_size(const dsv4_kv4_attention_args *args);
+dsv4_status dsv4_kv4_attention(const dsv4_kv4_attention_args *args, void *workspace, size_t workspace_bytes,
+                               dsv4_stream stream);
+
+/* ------------------------------------------------------------------------------------
  * Host helpers (no device work). */
 
 /* Readable name of a status code (static storage). */
