@@ -31,8 +31,7 @@
 // A value block with scale 255 (NaN) counts as zero in the product; the smallest such position is
 // noted per block of channels and rows that see it become NaN at the end, so that a row for which
 // the position is masked is not touched by it.
-#include "common.cuh"
-#include "kv4.h"
+#include "kv4_device.cuh"
 
 namespace dsv4 {
 
@@ -52,30 +51,6 @@ struct AttnParams {
 };
 
 // ---------------------------------------------------------------- the line of work
-
-// new tokens and positions of sequence s; false (and d_status) where they make no sense
-struct Seq {
-  int tok0, len, start, n;  // first token, new tokens, first position, positions to read
-};
-__device__ __forceinline__ bool seq_info(const Kv4AttnLaunch &p, int s, Seq *q, bool tell) {
-  const int64_t c0 = p.cu_seqlens[s], c1 = p.cu_seqlens[s + 1], st = p.start_pos[s];
-  const int64_t cap = static_cast<int64_t>(p.cache.max_blocks) * DSV4_PAGE_POSITIONS;
-  if (c0 < 0 || c1 < c0 || c1 > p.T || st < 0) {
-    if (tell) report(p.d_status, DSV4_DEV_BAD_LENGTH);
-    return false;
-  }
-  if (c1 == c0) return false;
-  int64_t n = st + (c1 - c0);
-  if (n > cap) {
-    if (tell) report(p.d_status, DSV4_DEV_BAD_LENGTH);
-    n = cap;
-  }
-  q->tok0 = static_cast<int>(c0);
-  q->len = static_cast<int>(c1 - c0);
-  q->start = static_cast<int>(st < cap ? st : cap);  // (a row behind the capacity sees what there is)
-  q->n = static_cast<int>(n);
-  return true;
-}
 
 struct Line {
   const Kv4AttnLaunch *p;
@@ -205,28 +180,6 @@ __device__ __forceinline__ int slices(int64_t all, int ctas) {
 
 // ---------------------------------------------------------------- fragments
 
-// a byte of two e2m1 codes -> fp16 pair; four bytes at once
-__device__ __forceinline__ void e2m1x8_to_half2(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-// scale byte -> 2^(byte - 127) as float (255: NaN)
-__device__ __forceinline__ float scale_value(uint32_t b) {
-  return __uint_as_float(b << 23 | (b == 255u ? 0x400000u : 0u));
-}
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -667,6 +620,9 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const __gr
   }
 }
 
+// Whether the tensor-core form for 256-row blocks takes the call.
+bool prompt_rows(const Kv4AttnLaunch &p) { return static_cast<int64_t>(p.max_new) * (p.Hq / p.Hk) > 64; }
+
 // rows of a tile: one tile of 8 where the rows of a sequence fit, two otherwise
 int tile_rows(const Kv4AttnLaunch &p) { return static_cast<int64_t>(p.max_new) * (p.Hq / p.Hk) <= 8 ? 8 : 16; }
 int resident(int R) { return R == 8 ? 3 : 2; }
@@ -690,6 +646,7 @@ size_t kv4_attention_workspace_bytes(const Kv4AttnLaunch &p) {
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnLaunch &q, void *ws, cudaStream_t st) {
+  if (prompt_rows(q)) return launch_kv4_prompt(q, st);
   AttnParams P{};
   P.a = q;
   const int R = tile_rows(q);

@@ -1,0 +1,56 @@
+// Device code that the attention kernels over the 4-bit key/value cache share.
+#pragma once
+
+#include "common.cuh"
+#include "kv4.h"
+
+namespace dsv4 {
+
+// new tokens and positions of sequence s; false (and d_status) where they make no sense
+struct Seq {
+  int tok0, len, start, n;  // first token, new tokens, first position, positions to read
+};
+__device__ __forceinline__ bool seq_info(const Kv4AttnLaunch &p, int s, Seq *q, bool tell) {
+  const int64_t c0 = p.cu_seqlens[s], c1 = p.cu_seqlens[s + 1], st = p.start_pos[s];
+  const int64_t cap = static_cast<int64_t>(p.cache.max_blocks) * DSV4_PAGE_POSITIONS;
+  if (c0 < 0 || c1 < c0 || c1 > p.T || st < 0) {
+    if (tell) report(p.d_status, DSV4_DEV_BAD_LENGTH);
+    return false;
+  }
+  if (c1 == c0) return false;
+  int64_t n = st + (c1 - c0);
+  if (n > cap) {
+    if (tell) report(p.d_status, DSV4_DEV_BAD_LENGTH);
+    n = cap;
+  }
+  q->tok0 = static_cast<int>(c0);
+  q->len = static_cast<int>(c1 - c0);
+  q->start = static_cast<int>(st < cap ? st : cap);  // (a row behind the capacity sees what there is)
+  q->n = static_cast<int>(n);
+  return true;
+}
+
+// a byte of two e2m1 codes -> fp16 pair; four bytes at once
+__device__ __forceinline__ void e2m1x8_to_half2(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// scale byte -> 2^(byte - 127) as float (255: NaN)
+__device__ __forceinline__ float scale_value(uint32_t b) {
+  return __uint_as_float(b << 23 | (b == 255u ? 0x400000u : 0u));
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+}  // namespace dsv4

@@ -1,0 +1,494 @@
+// Attention over the 4-bit key/value cache, rows in tiles of 256: prompts and pieces of them.
+//
+// The same operation as kv4_attention.cu's step kernel (there the formulas), for calls whose
+// sequences bring many rows (new tokens x query heads of a key/value head): bound by the tensor
+// cores and by the exponentials, not by memory. A CTA takes 256 rows of one key/value head of one
+// sequence, as two tiles of 128, and walks over the keys 128 at a time:
+//   warps 0-3, 4-7   softmax of row tile 0 and 1, one row per thread
+//   warps 8-11       codes -> fp16 K and V tiles in shared memory (128B swizzle, two stages)
+//   warp 12          one thread issues tcgen05.mma (kind::f16, M = 128):
+//                    S = Q K^T (Q, K from shared memory, S in TMEM) and
+//                    O += P V  (P in TMEM over S's columns, V from shared memory)
+// TMEM is full: S (128 columns) and O (D) of both row tiles. The two tiles alternate, so that one
+// tile's products run while the other's softmax does. The conversion of a K and V tile
+// (exact, see kv4_attention.cu) is shared by both row tiles: 2 x 128 x D codes against 4 x 128 x 128 x D
+// multiply-adds.
+// Softmax: the reference R that weights are taken against is raised (and O scaled) only when a
+// tile's maximum exceeds it by more than 2^8; weights are held times 2^7, at most 2^15 in fp16.
+// The S row is read twice from TMEM, for the maximum and for the weights, instead of being kept in
+// 128 registers.
+#include "kv4_device.cuh"
+
+namespace dsv4 {
+
+namespace {
+
+constexpr int kRows = 128;             // rows of a row tile
+constexpr int kKeys = 128;             // keys of a stage
+constexpr int kPThreads = 416;         // 13 warps
+constexpr float kRaise = 8.f;          // log2 that a maximum may exceed the reference by
+constexpr float kPOffP = 7.f;          // weights are held times 2^7
+
+struct PromptParams {
+  Kv4AttnLaunch a;
+  int row_blocks;  // blocks of 256 rows along the grid
+};
+
+template <int D>
+struct alignas(1024) PromptSmem {
+  static constexpr int kBlk = kKeys * 128;  // 128 rows x 64 channels
+  uint8_t q[2][D / 64][kBlk];
+  uint8_t k[2][D / 64][kBlk];
+  uint8_t v[2][D / 64][kBlk];
+  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], mma_done;
+  uint32_t tmem_base;
+  int abort_flag;
+  int bad[4];                  // the tile's page does not exist (tile index mod 4)
+  int nan_at[D / kKv4Block];   // smallest position with a NaN value block
+};
+
+// tcgen05.mma with A in TMEM
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// the unit of a CTA: rows 256 rb .. of one key/value head of one sequence
+struct PromptUnit {
+  Seq q;
+  int G, kvh;
+  int64_t row0, rows;  // first row, rows of the sequence
+  __device__ __forceinline__ int limit(int64_t row) const {  // positions that the row sees (0: no such row)
+    if (row >= rows) return 0;
+    return min(q.n, q.start + static_cast<int>(row / G) + 1);
+  }
+  // tiles of keys that row tile t reads
+  __device__ __forceinline__ int tiles(int t) const {
+    const int64_t first = row0 + t * kRows;
+    if (first >= rows) return 0;
+    return (limit(min(first + kRows, rows) - 1) + kKeys - 1) / kKeys;
+  }
+};
+
+template <int D>
+__device__ void convert_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const PromptUnit &u, int s, int T, int count,
+                             bool &dead) {
+  constexpr int W = D / 32;  // 16-byte pieces of a row's codes
+  const int r = threadIdx.x - 256, lane = threadIdx.x & 31;
+  const int32_t *table = p.cache.block_table + static_cast<int64_t>(s) * p.cache.max_blocks;
+  uint4 kc[W], vc[W];
+  uint32_t ks = 0, vs = 0;
+  bool bad = false;
+  auto load = [&](int j) {
+    const int page = table[j / (DSV4_PAGE_POSITIONS / kKeys)];
+    bad = page < 0 || page >= p.cache.num_pages;
+    if (bad) {
+      if (r == 0) report(p.d_status, DSV4_DEV_BAD_PAGE);
+#pragma unroll
+      for (int i = 0; i < W; ++i) kc[i] = vc[i] = make_uint4(0, 0, 0, 0);
+      ks = vs = 0;
+      return;
+    }
+    const int64_t row = (static_cast<int64_t>(page) * p.Hk + u.kvh) * DSV4_PAGE_POSITIONS +
+                        j % (DSV4_PAGE_POSITIONS / kKeys) * kKeys + r;
+    const uint4 *ksrc = reinterpret_cast<const uint4 *>(p.cache.k_codes + row * (D / 2));
+    const uint4 *vsrc = reinterpret_cast<const uint4 *>(p.cache.v_codes + row * (D / 2));
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) kc[i] = ksrc[i], vc[i] = vsrc[i];
+    if constexpr (D == 128) {
+      ks = *reinterpret_cast<const uint32_t *>(p.cache.k_scales + row * 4);
+      vs = *reinterpret_cast<const uint32_t *>(p.cache.v_scales + row * 4);
+    } else {
+      ks = *reinterpret_cast<const uint16_t *>(p.cache.k_scales + row * 2);
+      vs = *reinterpret_cast<const uint16_t *>(p.cache.v_scales + row * 2);
+    }
+  };
+  auto write = [&](uint8_t(&dst)[D / 64][PromptSmem<D>::kBlk], const uint4(&c)[W], uint32_t sc) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {  // piece i: channels 32 i .. 32 i + 31, one scale
+      const float f = scale_value(sc >> (8 * i) & 255u);
+      const uint32_t f2 = pack_half2(f, f);
+      const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t h[4];
+        e2m1x8_to_half2(w[k], h);
+        *reinterpret_cast<uint4 *>(&dst[i / 2][sw128_offset(r, i % 2 * 4 + k)]) =
+            make_uint4(hmul2(h[0], f2), hmul2(h[1], f2), hmul2(h[2], f2), hmul2(h[3], f2));
+      }
+    }
+  };
+  if (T > 0) load(0);
+  for (int j = 0; j < T; ++j, ++count) {
+    uint4 k0[W], v0[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) k0[i] = kc[i], v0[i] = vc[i];
+    const uint32_t ks0 = ks;
+    uint32_t vs0 = vs;
+    const bool bad0 = bad;
+    if (j + 1 < T) load(j + 1);
+    const int st = count & 1;
+    if (dead) continue;
+    bool ok = count < 2 || mbar_wait(&S.k_empty[st], (count / 2 - 1) & 1, &S.abort_flag);
+    if (!__all_sync(0xFFFFFFFFu, ok)) {
+      dead = true;
+      continue;
+    }
+    write(S.k[st], k0, ks0);
+    if (r == 0) S.bad[count & 3] = bad0;
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.k_full[st]);
+    const int key = j * kKeys + r;
+    if (key >= u.q.n) {
+      vs0 = 0;  // not a position of the sequence: 2^-127, zero in fp16
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if ((vs0 >> (8 * i) & 255u) == 255u) {
+          atomicMin(&S.nan_at[i], key);
+          vs0 &= ~(255u << (8 * i));
+        }
+    }
+    ok = count < 2 || mbar_wait(&S.v_empty[st], (count / 2 - 1) & 1, &S.abort_flag);
+    if (!__all_sync(0xFFFFFFFFu, ok)) {
+      dead = true;
+      continue;
+    }
+    write(S.v[st], v0, vs0);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.v_full[st]);
+  }
+}
+
+// T0 and T1: tiles of the two row tiles; kv: tiles of the CTA's units before; the counts run on over them
+template <int D>
+__device__ void mma_role(PromptSmem<D> &S, uint32_t tmem, int T0, int T1, int kv, int (&done)[2], int &units, bool &dead) {
+  const uint32_t id_s = idesc_f16(kRows, kKeys, 0, 0), id_o = idesc_f16(kRows, D, 0, 1);
+  constexpr uint32_t kB = PromptSmem<D>::kBlk;
+  const int T = max(T0, T1), Tq[2] = {T0, T1};
+  auto wait = [&](uint64_t *bar, int phase) {
+    if (!dead && !mbar_wait(bar, static_cast<uint32_t>(phase & 1), &S.abort_flag)) dead = true;
+    return !dead;
+  };
+  auto issue_s = [&](int t, int st) {
+    tc_fence_after();
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const uint64_t a = sw128_desc(smem_u32(S.q[t][kk / 4]), 16, 1024) + 2 * (kk & 3);
+      const uint64_t b = sw128_desc(smem_u32(S.k[st][kk / 4]), 16, 1024) + 2 * (kk & 3);
+      mma_bf16(tmem + 128u * t, a, b, id_s, kk > 0 ? 1u : 0u);
+    }
+    mma_commit(&S.s_full[t]);
+  };
+  auto issue_o = [&](int t, int st, bool acc) {
+    tc_fence_after();
+#pragma unroll
+    for (int kk = 0; kk < kKeys / 16; ++kk)
+      mma_f16_ts(tmem + 256u + static_cast<uint32_t>(D * t), tmem + 128u * t + 8u * kk,
+                 sw128_desc(smem_u32(S.v[st][0]) + kk * 2048, kB, 1024), id_o, acc || kk > 0 ? 1u : 0u);
+    mma_commit(&S.o_done[t]);
+  };
+  if (T == 0 || !wait(&S.q_full, units) || !wait(&S.k_full[kv & 1], kv / 2)) {
+    return;
+  }
+  for (int t = 0; t < 2; ++t)
+    if (Tq[t] > 0) issue_s(t, kv & 1);
+  mma_commit(&S.k_empty[kv & 1]);
+  for (int j = 0; j < T && !dead; ++j) {
+    const int st = (kv + j) & 1, nx = (kv + j + 1) & 1;
+    if (!wait(&S.v_full[st], (kv + j) / 2)) break;
+    for (int t = 0; t < 2; ++t) {
+      if (j < Tq[t]) {
+        if (!wait(&S.p_full[t], done[t] + j)) break;
+        issue_o(t, st, j > 0);
+      }
+      if (t == 0 && j + 1 < T && !wait(&S.k_full[nx], (kv + j + 1) / 2)) break;
+      if (j + 1 < Tq[t]) issue_s(t, nx);
+    }
+    if (dead) break;
+    mma_commit(&S.v_empty[st]);
+    if (j + 1 < T) mma_commit(&S.k_empty[nx]);
+  }
+  ++units;
+  done[0] += T0;
+  done[1] += T1;
+}
+
+template <int D>
+__device__ void softmax_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const PromptUnit &u, uint32_t tmem, int t, int T,
+                             int kv, int &done, bool &dead) {
+  const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
+  const uint32_t lanes = static_cast<uint32_t>(threadIdx.x & 96) << 16;
+  const uint32_t s_at = tmem + 128u * t + lanes, o_at = tmem + 256u + static_cast<uint32_t>(D * t) + lanes;
+  const int64_t row = u.row0 + t * kRows + r;
+  const int lim = u.limit(row);
+  const int64_t index = (u.q.tok0 + row / u.G) * p.Hq + u.kvh * u.G + row % u.G;  // of rows that exist
+  // the query row: scaled by a power of two into fp16's range (see kv4_attention.cu)
+  float rs;
+  {
+    uint4 raw[D / 8];
+    const uint16_t *src = p.q + (u.q.tok0 + row / u.G) * p.q_stride + static_cast<int64_t>(u.kvh * u.G + row % u.G) * D;
+    uint32_t am = 0;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      raw[i] = lim > 0 ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0, 0, 0, 0);
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) am = max(am, max((w[k] << 16) & 0x7FFF0000u, w[k] & 0x7FFF0000u));
+    }
+    const int ex = static_cast<int>(am >> 23) - 127;
+    const int sh = (am == 0 || ex >= 128) ? 0 : min(max(14 - ex, -113), 120);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      uint32_t h[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        h[k] = pack_half2(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
+      *reinterpret_cast<uint4 *>(&S.q[t][i / 8][sw128_offset(r, i % 8)]) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+    rs = p.softmax_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&S.q_full);
+
+  float R = -INFINITY, l0 = 0.f, l1 = 0.f;
+  // positions that every row of the warp sees (rows that do not exist see none and are not asked)
+  const int least = __reduce_min_sync(0xFFFFFFFFu, row < u.rows ? lim : 0x7FFFFFFF);
+  for (int j = 0; j < T; ++j) {
+    if (dead) break;
+    const bool ok = mbar_wait(&S.s_full[t], (done + j) & 1, &S.abort_flag);
+    if (!__all_sync(0xFFFFFFFFu, ok)) {
+      dead = true;
+      break;
+    }
+    tc_fence_after();
+    const int key0 = j * kKeys;
+    const bool edge = key0 + kKeys > least;
+    const bool bad = S.bad[(kv + j) & 3];
+    const int vis = bad ? 0 : lim - key0;  // columns that the row sees
+    float mx = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < kKeys; c += 64) {
+      uint32_t a[32], b[32];
+      tmem_ld32(s_at + c, a);
+      tmem_ld32(s_at + c + 32, b);
+      tmem_ld_wait();
+      if (edge || bad) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          if (c + i < vis) mx = fmaxf(mx, __uint_as_float(a[i]));
+          if (c + 32 + i < vis) mx = fmaxf(mx, __uint_as_float(b[i]));
+        }
+      } else {
+        float m1 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          mx = fmaxf(mx, __uint_as_float(a[i]));
+          m1 = fmaxf(m1, __uint_as_float(b[i]));
+        }
+        mx = fmaxf(mx, m1);
+      }
+    }
+    const float z = mx * rs;
+    const bool raise = z > R + kRaise || (R == -INFINITY && z > R);
+    if (__any_sync(0xFFFFFFFFu, raise)) {
+      const float f = raise ? ex2_approx(R - z) : 1.f;  // (R = -inf: zero)
+      if (raise) R = z;
+      l0 *= f;
+      l1 *= f;
+      if (j > 0) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&S.o_done[t], (done + j - 1) & 1, &S.abort_flag))) {
+          dead = true;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(o_at + c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+          tmem_st32(o_at + c, o);
+        }
+      }
+    }
+    const float off = R == -INFINITY ? 0.f : kPOffP - R;
+#pragma unroll
+    for (int c = 0; c < kKeys; c += 64) {
+      uint32_t a[32], b[32], w[32];
+      tmem_ld32(s_at + c, a);
+      tmem_ld32(s_at + c + 32, b);
+      tmem_ld_wait();
+      if (edge || bad) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          if (c + i >= vis) a[i] = 0xFF800000u;
+          if (c + 32 + i >= vis) b[i] = 0xFF800000u;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float p0 = ex2_approx(fmaf(__uint_as_float(a[2 * i]), rs, off));
+        const float p1 = ex2_approx(fmaf(__uint_as_float(a[2 * i + 1]), rs, off));
+        const float p2 = ex2_approx(fmaf(__uint_as_float(b[2 * i]), rs, off));
+        const float p3 = ex2_approx(fmaf(__uint_as_float(b[2 * i + 1]), rs, off));
+        l0 += p0 + p2;
+        l1 += p1 + p3;
+        w[i] = pack_half2(p0, p1);
+        w[16 + i] = pack_half2(p2, p3);
+      }
+      tmem_st32(s_at + c / 2, w);
+    }
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.p_full[t]);
+  }
+  if (T > 0 && !dead) {
+    const bool ok = mbar_wait(&S.o_done[t], (done + T - 1) & 1, &S.abort_flag);
+    if (__all_sync(0xFFFFFFFFu, ok)) {
+      tc_fence_after();
+      const float l = l0 + l1;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_at + c, o);
+        tmem_ld_wait();
+        const float nan = S.nan_at[c / kKv4Block] < lim ? __uint_as_float(0x7FC00000u) : 1.f;
+        if (lim > 0) {
+          uint4 *dst = reinterpret_cast<uint4 *>(p.out + index * D + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv * nan,
+                                 __uint_as_float(o[8 * i + 2 * k + 1]) * inv * nan);
+            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      tc_fence_before();
+      if (lim > 0 && p.lse) p.lse[index] = l == 0.f ? -INFINITY : (R - kPOffP + log2f(l)) * 0.6931471805599453f;
+    } else {
+      dead = true;
+    }
+  }
+  done += T;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_constant__ PromptParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  PromptSmem<D> &S = *reinterpret_cast<PromptSmem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const Kv4AttnLaunch &p = P.a;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  constexpr uint32_t kCols = 512;
+  // Blocks of later rows (more keys) come first; the sequences and heads of one block of rows are neighbours.
+  const int units = p.B * p.Hk;
+  const int first_rb = P.row_blocks - 1 - static_cast<int>(blockIdx.x) / units;
+  const int s = static_cast<int>(blockIdx.x) % units / p.Hk, kvh = static_cast<int>(blockIdx.x) % units % p.Hk;
+  if (tid == 0) {
+    mbar_init(&S.q_full, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.k_full[i], 4);
+      mbar_init(&S.k_empty[i], 1);
+      mbar_init(&S.v_full[i], 4);
+      mbar_init(&S.v_empty[i], 1);
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.p_full[i], 4);
+      mbar_init(&S.o_done[i], 1);
+    }
+    mbar_init(&S.mma_done, 1);
+    S.abort_flag = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  PromptUnit u;
+  u.G = p.Hq / p.Hk;
+  u.kvh = kvh;
+  const bool any = seq_info(p, s, &u.q, tid == 0);
+  u.rows = any ? static_cast<int64_t>(u.q.len) * u.G : 0;
+  if (static_cast<int64_t>(first_rb) * 2 * kRows >= u.rows) {
+    pdl_launch_dependents();
+    return;
+  }
+  if (warp == 12) {
+    tmem_alloc(&S.tmem_base, kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // (not before the TMEM is held: a following kernel's CTA that took it while waiting for this grid
+  // would wait for ever)
+  pdl_launch_dependents();
+  const uint32_t tmem = S.tmem_base;
+
+  int kv = 0, n_units = 0, done[2] = {0, 0}, mine = 0;
+  bool dead = false;
+  // (more than one turn only where a sequence brings more new tokens than the call's max_new says)
+  for (int64_t rb = first_rb; rb * 2 * kRows < u.rows; rb += P.row_blocks) {
+    u.row0 = rb * 2 * kRows;
+    const int T0 = u.tiles(0), T1 = u.tiles(1), T = max(T0, T1);
+    if (tid < D / kKv4Block) S.nan_at[tid] = 0x7FFFFFFF;
+    __syncthreads();
+    if (warp < 8) {
+      softmax_role<D>(p, S, u, tmem, warp / 4, warp < 4 ? T0 : T1, kv, mine, dead);
+    } else if (warp < 12) {
+      convert_role<D>(p, S, u, s, T, kv, dead);
+    } else if (tid == 384) {
+      mma_role<D>(S, tmem, T0, T1, kv, done, n_units, dead);
+    }
+    kv += T;
+    __syncthreads();
+  }
+  if (tid == 384) {  // every MMA issued here completes before the TMEM is freed
+    mma_commit(&S.mma_done);
+    volatile int dummy = 0;
+    mbar_wait(&S.mma_done, 0u, &dummy);
+  }
+  if (tid == 0 && S.abort_flag) report(p.d_status, DSV4_DEV_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
+}
+
+template <int D>
+cudaError_t launch_typed(const PromptParams &P, cudaStream_t st) {
+  const size_t smem = sizeof(PromptSmem<D>) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(kv4_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kv4_prompt_kernel<D>, dim3(static_cast<unsigned>(P.row_blocks) * P.a.B * P.a.Hk), dim3(kPThreads),
+                    smem, st, 1, P);
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_prompt(const Kv4AttnLaunch &q, cudaStream_t st) {
+  PromptParams P{};
+  P.a = q;
+  // blocks of 256 rows of the longest sequence; the grid has at most 2^30 CTAs (a CTA walks on over the rest)
+  const int64_t most = q.max_new < q.T ? q.max_new : q.T;
+  int64_t blocks = (most * (q.Hq / q.Hk) + 2 * kRows - 1) / (2 * kRows);
+  const int64_t room = (int64_t(1) << 30) / (static_cast<int64_t>(q.B) * q.Hk);
+  if (blocks > room) blocks = room;
+  if (blocks < 1) blocks = 1;
+  P.row_blocks = static_cast<int>(blocks);
+  return q.D == 64 ? launch_typed<64>(P, st) : launch_typed<128>(P, st);
+}
+
+}  // namespace dsv4
