@@ -6,6 +6,25 @@
 
 namespace dsv4 {
 
+// mbar_wait for hand-overs that take a fraction of a microsecond: no sleep between probes (the probe
+// itself holds the thread for a while), the abort flag and the clock only now and then.
+__device__ __forceinline__ bool mbar_spin(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    const uint64_t now = globaltimer();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+
 // new tokens and positions of sequence s; false (and d_status) where they make no sense
 struct Seq {
   int tok0, len, start, n;  // first token, new tokens, first position, positions to read

@@ -6,7 +6,7 @@
 // sequence, as two tiles of 128, and walks over the keys 128 at a time:
 //   warps 0-3, 4-7   softmax of row tile 0 and 1, one row per thread
 //   warps 8-11       codes -> fp16 K and V tiles in shared memory (128B swizzle, two stages)
-//   warp 12          one thread issues tcgen05.mma (kind::f16, M = 128):
+//   warp 12          issues tcgen05.mma (kind::f16, M = 128):
 //                    S = Q K^T (Q, K from shared memory, S in TMEM) and
 //                    O += P V  (P in TMEM over S's columns, V from shared memory)
 // TMEM is full: S (128 columns) and O (D) of both row tiles. The two tiles alternate, so that one
@@ -15,8 +15,8 @@
 // multiply-adds.
 // Softmax: the reference R that weights are taken against is raised (and O scaled) only when a
 // tile's maximum exceeds it by more than 2^8; weights are held times 2^7, at most 2^15 in fp16.
-// The S row is read twice from TMEM, for the maximum and for the weights, instead of being kept in
-// 128 registers.
+// A thread keeps its S row in 128 registers between the maximum and the weights (the warpgroups'
+// registers are split 184, 184, 96, 48), and hands its weights over in halves of 64 keys.
 #include "kv4_device.cuh"
 
 namespace dsv4 {
@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kRows = 128;             // rows of a row tile
 constexpr int kKeys = 128;             // keys of a stage
-constexpr int kPThreads = 416;         // 13 warps
+constexpr int kPThreads = 512;         // 4 warpgroups
 constexpr float kRaise = 8.f;          // log2 that a maximum may exceed the reference by
 constexpr float kPOffP = 7.f;          // weights are held times 2^7
 
@@ -40,20 +40,68 @@ struct alignas(1024) PromptSmem {
   uint8_t q[2][D / 64][kBlk];
   uint8_t k[2][D / 64][kBlk];
   uint8_t v[2][D / 64][kBlk];
-  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], mma_done;
+  uint64_t q_full, k_full[2], v_full[2], kv_empty[2], s_full[2], p_full[2][2], o_done[2], mma_done;
   uint32_t tmem_base;
   int abort_flag;
   int bad[4];                  // the tile's page does not exist (tile index mod 4)
   int nan_at[D / kKv4Block];   // smallest position with a NaN value block
 };
 
-// tcgen05.mma with A in TMEM
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// tcgen05.mma with A in TMEM, issued where en != 0 (by predicate: the warp stays together, so the
+// operands can sit in uniform registers; one thread in a branch of its own took about 120 cycles per
+// instruction to issue them, twice what one takes to run)
+__device__ __forceinline__ void mma_f16_ts_if(uint32_t en, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(en)
       : "memory");
+}
+
+// pairs of floats in one register pair, one instruction for both
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// 32 lanes x 32 bits, 16 consecutive columns
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xFFFFFFFFu, x); }
+
+// Registers of a warpgroup: the launch gives 512 threads x 128; softmax 2 x 184 + conversion 96 + products 48 = 4 x 128.
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // the unit of a CTA: rows 256 rb .. of one key/value head of one sequence
@@ -75,7 +123,7 @@ struct PromptUnit {
 
 template <int D>
 __device__ void convert_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const PromptUnit &u, int s, int T, int count,
-                             bool &dead) {
+                             int events, bool &dead) {
   constexpr int W = D / 32;  // 16-byte pieces of a row's codes
   const int r = threadIdx.x - 256, lane = threadIdx.x & 31;
   const int32_t *table = p.cache.block_table + static_cast<int64_t>(s) * p.cache.max_blocks;
@@ -132,11 +180,7 @@ __device__ void convert_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const Pro
     if (j + 1 < T) load(j + 1);
     const int st = count & 1;
     if (dead) continue;
-    bool ok = count < 2 || mbar_wait(&S.k_empty[st], (count / 2 - 1) & 1, &S.abort_flag);
-    if (!__all_sync(0xFFFFFFFFu, ok)) {
-      dead = true;
-      continue;
-    }
+    // (K's stage is free: its last product came before event j - 2, which V of tile j - 1 waited for)
     write(S.k[st], k0, ks0);
     if (r == 0) S.bad[count & 3] = bad0;
     fence_proxy_async_smem();
@@ -153,7 +197,10 @@ __device__ void convert_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const Pro
           vs0 &= ~(255u << (8 * i));
         }
     }
-    ok = count < 2 || mbar_wait(&S.v_empty[st], (count / 2 - 1) & 1, &S.abort_flag);
+    // events of a unit: 0 after S(0), j + 1 after PV(j) and S(j + 1); they take turns on two barriers, as one
+    // may be through before its predecessor is asked for
+    const int e = events + j - 1;
+    const bool ok = j < 1 || mbar_spin(&S.kv_empty[e & 1], (e >> 1) & 1, &S.abort_flag);
     if (!__all_sync(0xFFFFFFFFu, ok)) {
       dead = true;
       continue;
@@ -165,63 +212,76 @@ __device__ void convert_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const Pro
   }
 }
 
-// T0 and T1: tiles of the two row tiles; kv: tiles of the CTA's units before; the counts run on over them
+// The products, in the order PV0 S0 PV1 S1 of each tile j (S of tile j + 1), so that one row tile's run
+// beside the other's softmax. T0 and T1: tiles of the two row tiles; kv, done: tiles in the CTA's units
+// before. The whole warp runs this, lane 0 issues. An issue waits for the tensor pipe and every
+// hand-over costs some 150 cycles of it, so there are as few as the data needs: s_full also says
+// that the product before it (O up to the last tile) is done, and one event per tile frees V of tile j
+// and K of tile j + 1.
 template <int D>
-__device__ void mma_role(PromptSmem<D> &S, uint32_t tmem, int T0, int T1, int kv, int (&done)[2], int &units, bool &dead) {
-  const uint32_t id_s = idesc_f16(kRows, kKeys, 0, 0), id_o = idesc_f16(kRows, D, 0, 1);
+__device__ __forceinline__ void mma_role(PromptSmem<D> &S, uint32_t tmem, int T0, int T1, int kv, int (&done)[2], int units,
+                                         bool &dead) {
+  constexpr uint32_t id_s = idesc_f16(kRows, kKeys, 0, 0), id_o = idesc_f16(kRows, D, 0, 1);
   constexpr uint32_t kB = PromptSmem<D>::kBlk;
-  const int T = max(T0, T1), Tq[2] = {T0, T1};
+  const int T = max(T0, T1);
+  const uint32_t en = (threadIdx.x & 31) == 0;
   auto wait = [&](uint64_t *bar, int phase) {
-    if (!dead && !mbar_wait(bar, static_cast<uint32_t>(phase & 1), &S.abort_flag)) dead = true;
+    if (!dead) dead = !__all_sync(0xFFFFFFFFu, mbar_spin(bar, static_cast<uint32_t>(phase & 1), &S.abort_flag));
     return !dead;
   };
+  constexpr uint32_t kTileStep = (D / 64) * kB >> 4;  // descriptor units from one tile (q) or stage (k, v) to the next
+  const uint64_t qd = sw128_desc(smem_u32(S.q[0][0]), 16, 1024), kd = sw128_desc(smem_u32(S.k[0][0]), 16, 1024);
+  const uint64_t vd = sw128_desc(smem_u32(S.v[0][0]), kB, 1024);
   auto issue_s = [&](int t, int st) {
     tc_fence_after();
+    const uint64_t a0 = qd + t * kTileStep, b0 = kd + st * kTileStep;
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-      const uint64_t a = sw128_desc(smem_u32(S.q[t][kk / 4]), 16, 1024) + 2 * (kk & 3);
-      const uint64_t b = sw128_desc(smem_u32(S.k[st][kk / 4]), 16, 1024) + 2 * (kk & 3);
-      mma_bf16(tmem + 128u * t, a, b, id_s, kk > 0 ? 1u : 0u);
+      const uint32_t off = (kk / 4) * (kB >> 4) + 2 * (kk & 3);
+      mma_bf16_if(en, tmem + 128u * t, a0 + off, b0 + off, id_s, kk > 0 ? 1u : 0u);
     }
-    mma_commit(&S.s_full[t]);
+    mma_commit_if(en, &S.s_full[t]);
   };
-  auto issue_o = [&](int t, int st, bool acc) {
+  auto issue_o = [&](int t, int st, int half, bool acc) {
     tc_fence_after();
+    const uint32_t d = tmem + 256u + static_cast<uint32_t>(D * t), a0 = tmem + 128u * t + 32u * half;
+    const uint64_t b0 = vd + st * kTileStep + half * (kKeys / 2 * 128 >> 4);
 #pragma unroll
-    for (int kk = 0; kk < kKeys / 16; ++kk)
-      mma_f16_ts(tmem + 256u + static_cast<uint32_t>(D * t), tmem + 128u * t + 8u * kk,
-                 sw128_desc(smem_u32(S.v[st][0]) + kk * 2048, kB, 1024), id_o, acc || kk > 0 ? 1u : 0u);
-    mma_commit(&S.o_done[t]);
+    for (int i = 0; i < kKeys / 32; ++i)  // 16 keys: 8 columns of P, 2048 bytes of V
+      mma_f16_ts_if(en, d, a0 + 8u * i, b0 + i * (2048 >> 4), id_o, acc || i > 0 ? 1u : 0u);
   };
-  if (T == 0 || !wait(&S.q_full, units) || !wait(&S.k_full[kv & 1], kv / 2)) {
-    return;
-  }
-  for (int t = 0; t < 2; ++t)
-    if (Tq[t] > 0) issue_s(t, kv & 1);
-  mma_commit(&S.k_empty[kv & 1]);
-  for (int j = 0; j < T && !dead; ++j) {
-    const int st = (kv + j) & 1, nx = (kv + j + 1) & 1;
-    if (!wait(&S.v_full[st], (kv + j) / 2)) break;
+  if (T == 0 || !wait(&S.q_full, units) || !wait(&S.k_full[kv & 1], kv / 2)) return;
+  if (T0 > 0) issue_s(0, kv & 1);
+  if (T1 > 0) issue_s(1, kv & 1);
+  int e = kv + units;  // the unit's first event: each unit before had one more than tiles
+  mma_commit_if(en, &S.kv_empty[e & 1]);
+  if (!wait(&S.v_full[kv & 1], kv / 2)) return;
+  for (int j = 0; j < T; ++j) {
+    const int st = (kv + j) & 1, nx = st ^ 1;
+#pragma unroll
     for (int t = 0; t < 2; ++t) {
-      if (j < Tq[t]) {
-        if (!wait(&S.p_full[t], done[t] + j)) break;
-        issue_o(t, st, j > 0);
+      const int Tt = t == 0 ? T0 : T1;
+      if (j < Tt) {
+        if (!wait(&S.p_full[t][0], done[t] + j)) return;
+        issue_o(t, st, 0, j > 0);
+        if (!wait(&S.p_full[t][1], done[t] + j)) return;
+        issue_o(t, st, 1, true);
+        if (j + 1 == Tt) mma_commit_if(en, &S.o_done[t]);
       }
-      if (t == 0 && j + 1 < T && !wait(&S.k_full[nx], (kv + j + 1) / 2)) break;
-      if (j + 1 < Tq[t]) issue_s(t, nx);
+      if (t == 0 && j + 1 < T && !wait(&S.k_full[nx], (kv + j + 1) / 2)) return;
+      if (j + 1 < Tt) issue_s(t, nx);
     }
-    if (dead) break;
-    mma_commit(&S.v_empty[st]);
-    if (j + 1 < T) mma_commit(&S.k_empty[nx]);
+    ++e;
+    mma_commit_if(en, &S.kv_empty[e & 1]);
+    if (j + 1 < T && !wait(&S.v_full[nx], (kv + j + 1) / 2)) return;
   }
-  ++units;
   done[0] += T0;
   done[1] += T1;
 }
 
 template <int D>
 __device__ void softmax_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const PromptUnit &u, uint32_t tmem, int t, int T,
-                             int kv, int &done, bool &dead) {
+                             int kv, int &done, int &units, bool &dead) {
   const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
   const uint32_t lanes = static_cast<uint32_t>(threadIdx.x & 96) << 16;
   const uint32_t s_at = tmem + 128u * t + lanes, o_at = tmem + 256u + static_cast<uint32_t>(D * t) + lanes;
@@ -259,12 +319,13 @@ __device__ void softmax_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const Pro
   __syncwarp();
   if (lane == 0) mbar_arrive(&S.q_full);
 
-  float R = -INFINITY, l0 = 0.f, l1 = 0.f;
+  float R = -INFINITY;
+  uint64_t la = pack_f32x2(0.f, 0.f), lb = la;  // sums of the weights of every fourth pair of columns
   // positions that every row of the warp sees (rows that do not exist see none and are not asked)
   const int least = __reduce_min_sync(0xFFFFFFFFu, row < u.rows ? lim : 0x7FFFFFFF);
   for (int j = 0; j < T; ++j) {
     if (dead) break;
-    const bool ok = mbar_wait(&S.s_full[t], (done + j) & 1, &S.abort_flag);
+    const bool ok = mbar_spin(&S.s_full[t], (done + j) & 1, &S.abort_flag);
     if (!__all_sync(0xFFFFFFFFu, ok)) {
       dead = true;
       break;
@@ -274,42 +335,35 @@ __device__ void softmax_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const Pro
     const bool edge = key0 + kKeys > least;
     const bool bad = S.bad[(kv + j) & 3];
     const int vis = bad ? 0 : lim - key0;  // columns that the row sees
-    float mx = -INFINITY;
+    uint32_t a[4][32];
 #pragma unroll
-    for (int c = 0; c < kKeys; c += 64) {
-      uint32_t a[32], b[32];
-      tmem_ld32(s_at + c, a);
-      tmem_ld32(s_at + c + 32, b);
-      tmem_ld_wait();
-      if (edge || bad) {
+    for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, a[c]);
+    tmem_ld_wait();
+    if (edge || bad) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if (c + i < vis) mx = fmaxf(mx, __uint_as_float(a[i]));
-          if (c + 32 + i < vis) mx = fmaxf(mx, __uint_as_float(b[i]));
-        }
-      } else {
-        float m1 = -INFINITY;
+      for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          mx = fmaxf(mx, __uint_as_float(a[i]));
-          m1 = fmaxf(m1, __uint_as_float(b[i]));
-        }
-        mx = fmaxf(mx, m1);
-      }
+        for (int i = 0; i < 32; ++i)
+          if (32 * c + i >= vis) a[c][i] = 0xFF800000u;
     }
+    float mc[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      mc[c] = __uint_as_float(a[c][0]);
+#pragma unroll
+      for (int i = 1; i < 31; i += 2)
+        mc[c] = fmaxf(fmaxf(mc[c], __uint_as_float(a[c][i])), __uint_as_float(a[c][i + 1]));
+      mc[c] = fmaxf(mc[c], __uint_as_float(a[c][31]));
+    }
+    const float mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
     const float z = mx * rs;
     const bool raise = z > R + kRaise || (R == -INFINITY && z > R);
     if (__any_sync(0xFFFFFFFFu, raise)) {
       const float f = raise ? ex2_approx(R - z) : 1.f;  // (R = -inf: zero)
       if (raise) R = z;
-      l0 *= f;
-      l1 *= f;
-      if (j > 0) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&S.o_done[t], (done + j - 1) & 1, &S.abort_flag))) {
-          dead = true;
-          break;
-        }
-        tc_fence_after();
+      la = mul_f32x2(la, pack_f32x2(f, f));
+      lb = mul_f32x2(lb, pack_f32x2(f, f));
+      if (j > 0) {  // (s_full of tile j: the products of tile j - 1 are in O)
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -322,41 +376,35 @@ __device__ void softmax_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const Pro
       }
     }
     const float off = R == -INFINITY ? 0.f : kPOffP - R;
+    const uint64_t rs2 = pack_f32x2(rs, rs), off2 = pack_f32x2(off, off);
 #pragma unroll
-    for (int c = 0; c < kKeys; c += 64) {
-      uint32_t a[32], b[32], w[32];
-      tmem_ld32(s_at + c, a);
-      tmem_ld32(s_at + c + 32, b);
-      tmem_ld_wait();
-      if (edge || bad) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if (c + i >= vis) a[i] = 0xFF800000u;
-          if (c + 32 + i >= vis) b[i] = 0xFF800000u;
-        }
-      }
+    for (int c = 0; c < 4; ++c) {
+      uint32_t w[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float p0 = ex2_approx(fmaf(__uint_as_float(a[2 * i]), rs, off));
-        const float p1 = ex2_approx(fmaf(__uint_as_float(a[2 * i + 1]), rs, off));
-        const float p2 = ex2_approx(fmaf(__uint_as_float(b[2 * i]), rs, off));
-        const float p3 = ex2_approx(fmaf(__uint_as_float(b[2 * i + 1]), rs, off));
-        l0 += p0 + p2;
-        l1 += p1 + p3;
-        w[i] = pack_half2(p0, p1);
-        w[16 + i] = pack_half2(p2, p3);
+        float x0, x1;
+        unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(a[c][2 * i]), __uint_as_float(a[c][2 * i + 1])), rs2, off2), x0, x1);
+        x0 = ex2_approx(x0);
+        x1 = ex2_approx(x1);
+        if (i & 1) lb = add_f32x2(lb, pack_f32x2(x0, x1));
+        else la = add_f32x2(la, pack_f32x2(x0, x1));
+        w[i] = pack_half2(x0, x1);
       }
-      tmem_st32(s_at + c / 2, w);
+      tmem_st16(s_at + 16 * c, w);
+      if (c & 1) {
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.p_full[t][c / 2]);
+      }
     }
-    tmem_st_wait();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&S.p_full[t]);
   }
   if (T > 0 && !dead) {
-    const bool ok = mbar_wait(&S.o_done[t], (done + T - 1) & 1, &S.abort_flag);
+    const bool ok = mbar_spin(&S.o_done[t], units & 1, &S.abort_flag);
     if (__all_sync(0xFFFFFFFFu, ok)) {
       tc_fence_after();
+      float l0, l1;
+      unpack_f32x2(add_f32x2(la, lb), l0, l1);
       const float l = l0 + l1;
       const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
@@ -385,6 +433,7 @@ __device__ void softmax_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const Pro
     }
   }
   done += T;
+  if (T > 0) ++units;  // (units in which this row tile had rows)
 }
 
 template <int D>
@@ -392,7 +441,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
   extern __shared__ uint8_t smem_raw[];
   PromptSmem<D> &S = *reinterpret_cast<PromptSmem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const Kv4AttnLaunch &p = P.a;
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5);
   constexpr uint32_t kCols = 512;
   // Blocks of later rows (more keys) come first; the sequences and heads of one block of rows are neighbours.
   const int units = p.B * p.Hk;
@@ -402,11 +451,11 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
     mbar_init(&S.q_full, 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.k_full[i], 4);
-      mbar_init(&S.k_empty[i], 1);
       mbar_init(&S.v_full[i], 4);
-      mbar_init(&S.v_empty[i], 1);
+      mbar_init(&S.kv_empty[i], 1);
       mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.p_full[i], 4);
+      mbar_init(&S.p_full[i][0], 4);
+      mbar_init(&S.p_full[i][1], 4);
       mbar_init(&S.o_done[i], 1);
     }
     mbar_init(&S.mma_done, 1);
@@ -433,27 +482,49 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
   // (not before the TMEM is held: a following kernel's CTA that took it while waiting for this grid
   // would wait for ever)
   pdl_launch_dependents();
-  const uint32_t tmem = S.tmem_base;
+  const uint32_t tmem = __reduce_max_sync(0xFFFFFFFFu, S.tmem_base);
 
-  int kv = 0, n_units = 0, done[2] = {0, 0}, mine = 0;
+  // Every role walks over the CTA's units (more than one only where a sequence brings more new
+  // tokens than the call's max_new says) and meets the others before and after each.
+  int kv = 0;
   bool dead = false;
-  // (more than one turn only where a sequence brings more new tokens than the call's max_new says)
-  for (int64_t rb = first_rb; rb * 2 * kRows < u.rows; rb += P.row_blocks) {
-    u.row0 = rb * 2 * kRows;
-    const int T0 = u.tiles(0), T1 = u.tiles(1), T = max(T0, T1);
-    if (tid < D / kKv4Block) S.nan_at[tid] = 0x7FFFFFFF;
-    __syncthreads();
-    if (warp < 8) {
-      softmax_role<D>(p, S, u, tmem, warp / 4, warp < 4 ? T0 : T1, kv, mine, dead);
-    } else if (warp < 12) {
-      convert_role<D>(p, S, u, s, T, kv, dead);
-    } else if (tid == 384) {
-      mma_role<D>(S, tmem, T0, T1, kv, done, n_units, dead);
+  // (counts that steer loops pass through a warp reduction, whose result the compiler knows to be the
+  // same in all lanes: the issuing warp's operands then stay in uniform registers)
+  const int64_t blocks = (u.rows + 2 * kRows - 1) / (2 * kRows) - first_rb;
+  const int turns = uniform(static_cast<int>((blocks + P.row_blocks - 1) / P.row_blocks));
+  auto units_loop = [&](auto &&role) {
+    for (int turn = 0; turn < turns; ++turn) {
+      u.row0 = (first_rb + static_cast<int64_t>(turn) * P.row_blocks) * 2 * kRows;
+      const int T0 = uniform(u.tiles(0)), T1 = uniform(u.tiles(1));
+      if (tid < D / kKv4Block) S.nan_at[tid] = 0x7FFFFFFF;
+      __syncthreads();
+      role(T0, T1);
+      kv += max(T0, T1);
+      __syncthreads();
     }
-    kv += T;
-    __syncthreads();
+  };
+  if (warp < 8) {
+    more_registers<184>();
+    int done = 0, n_units = 0;
+    units_loop([&](int T0, int T1) {
+      softmax_role<D>(p, S, u, tmem, warp / 4, warp < 4 ? T0 : T1, kv, done, n_units, dead);
+    });
+  } else if (warp < 12) {
+    fewer_registers<96>();
+    int events = 0;  // of kv_empty in the units before
+    units_loop([&](int T0, int T1) {
+      convert_role<D>(p, S, u, s, max(T0, T1), kv, events, dead);
+      events += max(T0, T1) + 1;
+    });
+  } else {
+    fewer_registers<48>();
+    int n_units = 0, done[2] = {0, 0};
+    units_loop([&](int T0, int T1) {
+      if (warp == 12) mma_role<D>(S, tmem, T0, T1, kv, done, n_units, dead);
+      ++n_units;
+    });
   }
-  if (tid == 384) {  // every MMA issued here completes before the TMEM is freed
+  if (tid == 384) {  // every product issued here ends before the TMEM is freed
     mma_commit(&S.mma_done);
     volatile int dummy = 0;
     mbar_wait(&S.mma_done, 0u, &dummy);

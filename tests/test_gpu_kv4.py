@@ -13,8 +13,8 @@ Bounds, with u = 2^-24 (half a float32 step, relative):
   2 (D + 4) u S (sums of D terms in float32 whose adder may drop bits, twice the rounding), the weights by that
   and 2^-21 (the hardware's 2^x, the exponent's own rounding of at most 2u (S + |lse|) log2 e),
   and each weight is rounded to fp16 (2^-11 relative; below fp16's normal numbers, where the step is
-  2^-24, by 2^-25 absolute, and weights are held times 2^14, so by 2^-39 of the row's largest weight, which
-  is at most the sum of all). The output: (2^-11 + 2 eps) sum_j p_j |v_j| + 2^-39 sum_j |v_j| + 2^-8 |o|,
+  2^-24, by 2^-25 absolute; a row's largest weight is held as 2^7 or more, so by 2^-32 of it, which
+  is at most the sum of all). The output: (2^-11 + 2 eps) sum_j p_j |v_j| + 2^-32 sum_j |v_j| + 2^-8 |o|,
   lse: eps + 4u |lse| + 2^-21.
 """
 
@@ -280,7 +280,7 @@ def check_attention(c, q, lens, starts, out, lse, scale=None, sample=None, ctx="
             for i in rows:
                 want, wl, mag, top = K.attention(qv[at + i:at + i + 1], kk[:first + i + 1], vv[:first + i + 1], first + i, scale)
                 eps = 2 * (D + 4) * U * top + 2.0 ** -21 + 2 * U * 1.4427 * (top + np.abs(wl))
-                tiny = 2.0 ** -39 * np.repeat(np.abs(vv[:first + i + 1]).sum(0), q.shape[1] // c.kv_heads, 0)
+                tiny = 2.0 ** -32 * np.repeat(np.abs(vv[:first + i + 1]).sum(0), q.shape[1] // c.kv_heads, 0)
                 limit = (2.0 ** -11 + 2 * eps[..., None]) * mag + tiny + BF16 * np.abs(want) + 1e-30
                 err = np.abs(ov[at + i] - want[0])
                 assert np.all(err <= limit[0]), (ctx, s, i, (err / limit[0]).max())
