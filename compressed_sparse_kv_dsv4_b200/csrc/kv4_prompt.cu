@@ -47,14 +47,29 @@ struct alignas(1024) PromptSmem {
   int nan_at[D / kKv4Block];   // smallest position with a NaN value block
 };
 
-// tcgen05.mma with A in TMEM, issued where en != 0 (by predicate: the warp stays together, so the
-// operands can sit in uniform registers; one thread in a branch of its own took about 120 cycles per
-// instruction to issue them, twice what one takes to run)
-__device__ __forceinline__ void mma_f16_ts_if(uint32_t en, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// One lane of the warp. Through elect.sync the compiler knows that a single thread is inside the branch
+// and issues a product in few instructions; with "lane 0" as the condition (branch or predicate) an
+// issue took 75 to 170 cycles beside busy warps, more than the 64 that the product itself takes, with
+// elect.sync around each instruction 40 to 55.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
+// tcgen05.mma kind::f16, A and B in shared memory (descriptors that share their high word) or A in TMEM
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(en)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
 
@@ -214,7 +229,7 @@ __device__ void convert_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const Pro
 
 // The products, in the order PV0 S0 PV1 S1 of each tile j (S of tile j + 1), so that one row tile's run
 // beside the other's softmax. T0 and T1: tiles of the two row tiles; kv, done: tiles in the CTA's units
-// before. The whole warp runs this, lane 0 issues. An issue waits for the tensor pipe and every
+// before. The whole warp runs this, one lane issues. An issue waits for the tensor pipe and every
 // hand-over costs some 150 cycles of it, so there are as few as the data needs: s_full also says
 // that the product before it (O up to the last tile) is done, and one event per tile frees V of tile j
 // and K of tile j + 1.
@@ -224,37 +239,41 @@ __device__ __forceinline__ void mma_role(PromptSmem<D> &S, uint32_t tmem, int T0
   constexpr uint32_t id_s = idesc_f16(kRows, kKeys, 0, 0), id_o = idesc_f16(kRows, D, 0, 1);
   constexpr uint32_t kB = PromptSmem<D>::kBlk;
   const int T = max(T0, T1);
-  const uint32_t en = (threadIdx.x & 31) == 0;
   auto wait = [&](uint64_t *bar, int phase) {
     if (!dead) dead = !__all_sync(0xFFFFFFFFu, mbar_spin(bar, static_cast<uint32_t>(phase & 1), &S.abort_flag));
     return !dead;
   };
   constexpr uint32_t kTileStep = (D / 64) * kB >> 4;  // descriptor units from one tile (q) or stage (k, v) to the next
-  const uint64_t qd = sw128_desc(smem_u32(S.q[0][0]), 16, 1024), kd = sw128_desc(smem_u32(S.k[0][0]), 16, 1024);
-  const uint64_t vd = sw128_desc(smem_u32(S.v[0][0]), kB, 1024);
+  const uint64_t qd = sw128_desc(smem_u32(S.q[0][0]), 16, 1024), vd = sw128_desc(smem_u32(S.v[0][0]), kB, 1024);
+  const uint32_t q_lo = static_cast<uint32_t>(qd), q_hi = static_cast<uint32_t>(qd >> 32);
+  const uint32_t k_lo = static_cast<uint32_t>(sw128_desc(smem_u32(S.k[0][0]), 16, 1024));
+  const uint32_t v_lo = static_cast<uint32_t>(vd), v_hi = static_cast<uint32_t>(vd >> 32);
+  auto commit = [&](uint64_t *bar) {
+    if (elect_one()) mma_commit(bar);
+  };
   auto issue_s = [&](int t, int st) {
     tc_fence_after();
-    const uint64_t a0 = qd + t * kTileStep, b0 = kd + st * kTileStep;
+    const uint32_t a0 = q_lo + t * kTileStep, b0 = k_lo + st * kTileStep;
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
       const uint32_t off = (kk / 4) * (kB >> 4) + 2 * (kk & 3);
-      mma_bf16_if(en, tmem + 128u * t, a0 + off, b0 + off, id_s, kk > 0 ? 1u : 0u);
+      if (elect_one()) mma_ss(tmem + 128u * t, a0 + off, b0 + off, q_hi, id_s, kk > 0 ? 1u : 0u);
     }
-    mma_commit_if(en, &S.s_full[t]);
+    commit(&S.s_full[t]);
   };
-  auto issue_o = [&](int t, int st, int half, bool acc) {
+  auto issue_o = [&](int t, int st, int half, uint32_t acc) {
     tc_fence_after();
     const uint32_t d = tmem + 256u + static_cast<uint32_t>(D * t), a0 = tmem + 128u * t + 32u * half;
-    const uint64_t b0 = vd + st * kTileStep + half * (kKeys / 2 * 128 >> 4);
+    const uint32_t b0 = v_lo + st * kTileStep + half * (kKeys / 2 * 128 >> 4);
 #pragma unroll
     for (int i = 0; i < kKeys / 32; ++i)  // 16 keys: 8 columns of P, 2048 bytes of V
-      mma_f16_ts_if(en, d, a0 + 8u * i, b0 + i * (2048 >> 4), id_o, acc || i > 0 ? 1u : 0u);
+      if (elect_one()) mma_ts(d, a0 + 8u * i, b0 + i * (2048 >> 4), v_hi, id_o, i > 0 ? 1u : acc);
   };
   if (T == 0 || !wait(&S.q_full, units) || !wait(&S.k_full[kv & 1], kv / 2)) return;
   if (T0 > 0) issue_s(0, kv & 1);
   if (T1 > 0) issue_s(1, kv & 1);
   int e = kv + units;  // the unit's first event: each unit before had one more than tiles
-  mma_commit_if(en, &S.kv_empty[e & 1]);
+  commit(&S.kv_empty[e & 1]);
   if (!wait(&S.v_full[kv & 1], kv / 2)) return;
   for (int j = 0; j < T; ++j) {
     const int st = (kv + j) & 1, nx = st ^ 1;
@@ -263,16 +282,16 @@ __device__ __forceinline__ void mma_role(PromptSmem<D> &S, uint32_t tmem, int T0
       const int Tt = t == 0 ? T0 : T1;
       if (j < Tt) {
         if (!wait(&S.p_full[t][0], done[t] + j)) return;
-        issue_o(t, st, 0, j > 0);
+        issue_o(t, st, 0, j > 0 ? 1u : 0u);
         if (!wait(&S.p_full[t][1], done[t] + j)) return;
-        issue_o(t, st, 1, true);
-        if (j + 1 == Tt) mma_commit_if(en, &S.o_done[t]);
+        issue_o(t, st, 1, 1u);
+        if (j + 1 == Tt) commit(&S.o_done[t]);
       }
       if (t == 0 && j + 1 < T && !wait(&S.k_full[nx], (kv + j + 1) / 2)) return;
       if (j + 1 < Tt) issue_s(t, nx);
     }
     ++e;
-    mma_commit_if(en, &S.kv_empty[e & 1]);
+    commit(&S.kv_empty[e & 1]);
     if (j + 1 < T && !wait(&S.v_full[nx], (kv + j + 1) / 2)) return;
   }
   done[0] += T0;
@@ -524,8 +543,8 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
       ++n_units;
     });
   }
-  if (tid == 384) {  // every product issued here ends before the TMEM is freed
-    mma_commit(&S.mma_done);
+  if (warp == 12) {  // every product issued here ends before the TMEM is freed
+    if (elect_one()) mma_commit(&S.mma_done);
     volatile int dummy = 0;
     mbar_wait(&S.mma_done, 0u, &dummy);
   }
