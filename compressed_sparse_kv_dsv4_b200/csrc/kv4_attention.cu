@@ -12,11 +12,13 @@
 // parts of the others go through the workspace and kv4_combine_kernel joins them (a fixed
 // order, so results do not depend on timing).
 //
-// Inside a CTA a producer lane brings each tile of 64 keys into a ring of shared-memory stages
-// with four bulk copies (codes and scales of a head's rows are contiguous within a page), and
-// each of four warps takes every fourth tile whole: the products, an online softmax of its own and
-// the weighted sum of values, in registers; the warps' sums are joined at the end of the slice's
-// part of the unit. The matrix products are mma.sync m16n8k16 (fp16 operands, fp32 sums) with
+// Inside a CTA each of four warps takes every fourth tile whole: it brings its tiles into two or three
+// stages of its own with bulk copies (codes and scales of a head's rows are contiguous within a page), and
+// does the products, an online softmax of its own and the weighted sum of values in registers; the
+// warps' sums are joined at the end of the slice's part of the unit. With no producer between them the warps
+// meet only there, and sixteen of them fit an SM at 128 registers (what bounds the kernel is their
+// instructions, 1.2 a value, on the ALU pipe first: two conversions and a permute for 4 values).
+// The matrix products are mma.sync m16n8k16 (fp16 operands, fp32 sums) with
 // keys (S^T = K Q^T) and channels (O^T = V^T P^T) on the 16-row side and rows on the 8-column
 // side: a decode step has G rows, far fewer than a tcgen05 tile's 128, and the operand is made in
 // registers from 4-bit codes, where mma.sync takes it without a trip through shared memory.
@@ -37,9 +39,9 @@ namespace dsv4 {
 
 namespace {
 
-constexpr int kTile = 64;       // keys of a stage
-constexpr int kWarps = 4;       // consumer warps
-constexpr int kThreadsA = 32 * (kWarps + 1);
+constexpr int kTile = 64;       // keys of a warp's turn
+constexpr int kWarps = 4;
+constexpr int kThreadsA = 32 * kWarps;
 constexpr float kPOff = 14.f;   // weights are held times 2^14
 constexpr int kMinTiles = 4;    // tiles of a slice, at least (one per warp)
 
@@ -48,15 +50,21 @@ struct AttnParams {
   float *part_o;     // [2 slots][R][D] per CTA: unnormalised sums
   float2 *part_ml;   // [2 slots][R] per CTA: maximum (log2) and sum
   int ctas;
+  int group;         // query heads of a key/value head
 };
 
 // ---------------------------------------------------------------- the line of work
 
+// a / b where both are >= 0 and mostly below 2^32 (a 64-bit division takes some hundred instructions)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
 struct Line {
   const Kv4AttnLaunch *p;
-  int G, R;
+  int G, R, r_log2;  // rows of a tile: a power of two
   __device__ __forceinline__ int row_tiles(const Seq &q) const {
-    return static_cast<int>((static_cast<int64_t>(q.len) * G + R - 1) / R);
+    return static_cast<int>((static_cast<int64_t>(q.len) * G + R - 1) >> r_log2);
   }
   __device__ __forceinline__ int tiles(const Seq &q) const { return (q.n + kTile - 1) / kTile; }
   __device__ __forceinline__ int64_t weight(int s, bool tell = false) const {
@@ -126,10 +134,10 @@ struct Walk {
     seq_info(*ln.p, s, &q, false);
     row_tiles = ln.row_tiles(q);
     tiles = ln.tiles(q);
-    const int64_t unit = off / tiles;
-    tile = static_cast<int>(off % tiles);
-    kvh = static_cast<int>(unit / row_tiles);
-    rt = static_cast<int>(unit % row_tiles);
+    const int64_t unit = quotient(off, tiles), head = quotient(unit, row_tiles);
+    tile = static_cast<int>(off - unit * tiles);
+    kvh = static_cast<int>(head);
+    rt = static_cast<int>(unit - head * row_tiles);
   }
   // the part of the current unit that lies in the slice: tiles [tile, stop)
   __device__ __forceinline__ int stop() const {
@@ -154,27 +162,29 @@ struct Walk {
   // positions that any row of the unit sees
   __device__ __forceinline__ int unit_limit() const {
     const int64_t last = min(static_cast<int64_t>(q.len) * ln.G, static_cast<int64_t>(rt + 1) * ln.R) - 1;
-    return min(q.n, q.start + static_cast<int>(last / ln.G) + 1);
+    return min(q.n, q.start + static_cast<int>(quotient(last, ln.G)) + 1);
   }
   // positions that row r of the unit sees (0: there is no such row)
   __device__ __forceinline__ int row_limit(int r) const {
     const int64_t row = static_cast<int64_t>(rt) * ln.R + r;
     if (row >= static_cast<int64_t>(q.len) * ln.G) return 0;
-    return min(q.n, q.start + static_cast<int>(row / ln.G) + 1);
+    return min(q.n, q.start + static_cast<int>(quotient(row, ln.G)) + 1);
   }
   // [token][head] index of row r
   __device__ __forceinline__ int64_t row_index(int r) const {
     const int64_t row = static_cast<int64_t>(rt) * ln.R + r;
-    return (q.tok0 + row / ln.G) * ln.p->Hq + kvh * ln.G + row % ln.G;
+    const int64_t i = quotient(row, ln.G);
+    return (q.tok0 + i) * ln.p->Hq + kvh * ln.G + (row - i * ln.G);
   }
 };
 
 __device__ __forceinline__ int64_t slice_at(int64_t all, int ctas, int c) {
   // (all is at most 2^31 tokens' row tiles times 2^25 tiles; the quotient form stays in 64 bits)
-  return all / ctas * c + all % ctas * c / ctas;
+  const int64_t each = quotient(all, ctas);
+  return each * c + quotient((all - each * ctas) * c, ctas);
 }
 __device__ __forceinline__ int slices(int64_t all, int ctas) {
-  const int64_t most = (all + kMinTiles - 1) / kMinTiles;
+  const int64_t most = (all + kMinTiles - 1) / kMinTiles;  // (a shift)
   return most < ctas ? static_cast<int>(most) : ctas;
 }
 
@@ -198,48 +208,49 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
 __device__ __forceinline__ int key_of(int g) { return (g & 4) + ((0x2130 >> (4 * (g & 3))) & 3); }
 
 template <int D, int NT>
-struct StageBytes {
+struct StepShape {
   static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / kKv4Block;
-  static constexpr int kStage = 2 * (kCodes + kScales);
-  static constexpr int kStages = D == 128 ? (NT == 1 ? 6 : 8) : 8;
+  static constexpr int kHalf = kCodes + kScales;   // keys or values of a tile
+  static constexpr int kStages = D == 128 ? 3 : 4;  // of a warp, half a tile each
+  static constexpr int kResident = D * NT <= 128 ? 3 : 2;  // CTAs of an SM: 168 or 255 registers a thread
 };
 
 template <int D, int NT>
 struct alignas(128) AttnSmem {
-  using SB = StageBytes<D, NT>;
+  using Sh = StepShape<D, NT>;
   struct alignas(128) Stage {
-    uint8_t k[SB::kCodes], v[SB::kCodes], ks[SB::kScales], vs[SB::kScales];
-  } stage[SB::kStages];
+    uint8_t c[Sh::kCodes], s[Sh::kScales];
+  } stage[kWarps][Sh::kStages];
   float o[kWarps][8 * NT][D + 4];  // the warps' sums, joined at the end of a unit's part
   float2 ml[kWarps][8 * NT];
+  int64_t index[8 * NT];           // [token][head] of the unit's rows
+  int lim[8 * NT];                 // positions that they see (0: no such row)
   int64_t prefix[kThreadsA + 1], warp_sums[kThreadsA / 32];
-  uint64_t full[SB::kStages], empty[SB::kStages];
-  int bad[SB::kStages];            // the stage's page does not exist
+  uint64_t full[kWarps][Sh::kStages];
+  int bad[kWarps][Sh::kStages];    // the stage's page does not exist
   int nan_at[D / kKv4Block];       // smallest position with a NaN value block
   int abort_flag;
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreadsA, NT == 1 ? 3 : 2) kv4_step_kernel(const __grid_constant__ AttnParams P) {
+__global__ void __launch_bounds__(kThreadsA, StepShape<D, NT>::kResident)
+    kv4_step_kernel(const __grid_constant__ AttnParams P) {
   constexpr int R = 8 * NT, KS = D / 16, MT = kTile / 16;
-  using SB = StageBytes<D, NT>;
-  constexpr int NS = SB::kStages;
+  using Sh = StepShape<D, NT>;
+  constexpr int NS = Sh::kStages;
   extern __shared__ uint8_t smem_raw[];
   using Smem = AttnSmem<D, NT>;
   Smem &S = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   const Kv4AttnLaunch &p = P.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&S.full[i], 1);
-      mbar_init(&S.empty[i], 1);
-    }
+    for (int i = 0; i < kWarps * NS; ++i) mbar_init(&S.full[0][0] + i, 2);
     S.abort_flag = 0;
     fence_mbar_init();
   }
   pdl_wait();
   pdl_launch_dependents();
-  const Line line{&p, p.Hq / p.Hk, R};
+  const Line line{&p, P.group, R, 31 - __clz(R)};
   const int chunk = (p.B + kThreadsA - 1) / kThreadsA;
   const int64_t all = line_prefix(line, kThreadsA, chunk, S.prefix, S.warp_sums);
   const int ctas = slices(all, P.ctas);
@@ -247,57 +258,76 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 3 : 2) kv4_step_kernel(co
   const int64_t from = slice_at(all, ctas, blockIdx.x), to = slice_at(all, ctas, blockIdx.x + 1);
   Walk w;
   w.begin(line, S.prefix, kThreadsA, chunk, from, to);
+  fence_proxy_async_global();  // the cache's rows may come from the kernel before, by plain stores
 
-  if (warp == kWarps) {
-    // ---------------- producer
-    if (lane == 0) {
-      fence_proxy_async_global();  // the cache's rows may come from the kernel before, by plain stores
-      int issued = 0;
-      bool ok = true;
-      do {
-        const int stop = min(w.stop(), (w.unit_limit() + kTile - 1) / kTile);
-        const int32_t *table = p.cache.block_table + static_cast<int64_t>(w.s) * p.cache.max_blocks;
-        for (int t = w.tile; ok && t < stop; ++t) {
-          const int slot = issued % NS;
-          const int page = table[t / (DSV4_PAGE_POSITIONS / kTile)];
-          if (issued >= NS && !mbar_wait(&S.empty[slot], (issued / NS - 1) & 1, &S.abort_flag)) {
-            ok = false;
-            break;
-          }
-          const bool bad = page < 0 || page >= p.cache.num_pages;
-          S.bad[slot] = bad;
-          if (bad) {
-            report(p.d_status, DSV4_DEV_BAD_PAGE);
-            mbar_arrive(&S.full[slot]);
-          } else {
-            const int64_t row = (static_cast<int64_t>(page) * p.Hk + w.kvh) * DSV4_PAGE_POSITIONS +
-                                t % (DSV4_PAGE_POSITIONS / kTile) * kTile;
-            mbar_arrive_expect_tx(&S.full[slot], SB::kStage);
-            bulk_load(S.stage[slot].k, p.cache.k_codes + row * (D / 2), SB::kCodes, &S.full[slot]);
-            bulk_load(S.stage[slot].ks, p.cache.k_scales + row * (D / kKv4Block), SB::kScales, &S.full[slot]);
-            bulk_load(S.stage[slot].v, p.cache.v_codes + row * (D / 2), SB::kCodes, &S.full[slot]);
-            bulk_load(S.stage[slot].vs, p.cache.v_scales + row * (D / kKv4Block), SB::kScales, &S.full[slot]);
-          }
-          ++issued;
-        }
-      } while (w.next() && ok);
-      if (!ok || *static_cast<volatile int *>(&S.abort_flag)) {  // let the copies in flight land before the CTA leaves
-        for (int n = issued > NS ? NS : issued; n >= 1; --n) {
-          const int i = issued - n;
-          volatile int dummy = 0;
-          mbar_wait(&S.full[i % NS], (i / NS) & 1, &dummy);
-        }
+  const int g = lane >> 2, t4 = lane & 3;
+  uint32_t issued = 0, used = 0;  // this warp's tiles
+  bool dead = false;
+  // The warp's next half tile into its next stage: keys (half 0) or values of tile t of u's unit. Lane 0 copies the
+  // codes and lane 1 the scales, in the same instructions.
+  const uint32_t row_bytes = lane == 0 ? D / 2 : D / kKv4Block;
+  const uint8_t *const src_k = lane == 0 ? p.cache.k_codes : p.cache.k_scales;
+  const uint8_t *const src_v = lane == 0 ? p.cache.v_codes : p.cache.v_scales;
+  auto fetch = [&](const Walk &u, int t, int half) {
+    const uint32_t slot = issued % NS;
+    if (lane < 2) {
+      const int page = p.cache.block_table[static_cast<int64_t>(u.s) * p.cache.max_blocks + t / (DSV4_PAGE_POSITIONS / kTile)];
+      const bool bad = static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.cache.num_pages);
+      uint64_t *bar = &S.full[warp][slot];
+      S.bad[warp][slot] = bad;
+      if (bad) {
+        report(p.d_status, DSV4_DEV_BAD_PAGE);
+        mbar_arrive(bar);
+      } else {
+        const int64_t row = static_cast<int64_t>(page) * (p.Hk * DSV4_PAGE_POSITIONS) +
+                            (u.kvh * DSV4_PAGE_POSITIONS + t % (DSV4_PAGE_POSITIONS / kTile) * kTile);
+        typename Smem::Stage &T = S.stage[warp][slot];
+        mbar_arrive_expect_tx(bar, row_bytes * kTile);
+        bulk_load(lane == 0 ? T.c : T.s, (half ? src_v : src_k) + row * row_bytes, row_bytes * kTile, bar);
       }
     }
-    __syncwarp();
-  } else {
-    // ---------------- consumers
-    const int g = lane >> 2, t4 = lane & 3;
-    int done = 0;     // stages of the CTA before the current unit's part
-    bool dead = false;
-    do {
+    ++issued;
+  };
+  // tiles of the unit's part that any of its rows sees: [u.tile, ...); warp w takes the w-th, (w + 4)-th, ...
+  auto seen = [&](const Walk &u) { return max(min(u.stop(), (u.unit_limit() + kTile - 1) / kTile) - u.tile, 0); };
+  auto fetch_half = [&](const Walk &u, int count, int h) {  // half tile h of the warp's
+    const int i = warp + (h >> 1) * kWarps;
+    if (i < count) fetch(u, u.tile + i, h & 1);
+  };
+  auto fetch_first = [&](const Walk &u) {
+    const int count = seen(u);
+#pragma unroll
+    for (int h = 0; h < NS; ++h) fetch_half(u, count, h);
+  };
+  // waits for the warp's next stage; negative: gave up
+  auto arrived = [&]() -> int {
+    const uint32_t slot = used % NS;
+    const bool ok = !dead && mbar_spin(&S.full[warp][slot], (used / NS) & 1, &S.abort_flag);
+    if (!__all_sync(0xFFFFFFFFu, ok)) {
+      dead = true;
+      return -1;
+    }
+    ++used;
+    return static_cast<int>(slot);
+  };
+  bool first = true;
+  for (;;) {
       const int stop = w.stop(), limit = w.unit_limit();
-      const int vis = min(stop, (limit + kTile - 1) / kTile);
+      const int count = seen(w);
+      // lane r knows row r: the positions it sees (0: there is no such row) and where it is
+      int my_lim = 0, my_head = 0;
+      int64_t my_tok = 0;
+      if (lane < R) {
+        const int64_t row = (static_cast<int64_t>(w.rt) << line.r_log2) + lane;
+        if (row < static_cast<int64_t>(w.q.len) * line.G) {
+          const int64_t i = quotient(row, line.G);
+          my_lim = min(w.q.n, w.q.start + static_cast<int>(i) + 1);
+          my_tok = w.q.tok0 + i;
+          my_head = w.kvh * line.G + static_cast<int>(row - i * line.G);
+          if (warp == 0) S.index[lane] = my_tok * p.Hq + my_head;
+        }
+        if (warp == 0) S.lim[lane] = my_lim;
+      }
       // Q fragments: column g of tile nt is row 8 nt + g; a lane's channels of step j are D/4 t4 + 4 j ..+3
       uint32_t qf[NT][KS][2];
       float rs[NT][2];   // log2 score per product, of columns 2 t4 and 2 t4 + 1
@@ -305,24 +335,27 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 3 : 2) kv4_step_kernel(co
       int least = limit; // positions that every row sees
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int r = 8 * nt + g, rl = w.row_limit(r);
-        uint32_t raw[KS * 2];
-        uint32_t am = 0;
-        if (rl > 0) {
-          const int64_t row = static_cast<int64_t>(w.rt) * R + r;
-          const uint16_t *src = p.q + (w.q.tok0 + row / line.G) * p.q_stride +
-                                static_cast<int64_t>(w.kvh * line.G + row % line.G) * D + t4 * (D / 4);
+        const int rl = __shfl_sync(0xFFFFFFFFu, my_lim, 8 * nt + g);
+        const int64_t tok = __shfl_sync(0xFFFFFFFFu, my_tok, 8 * nt + g);
+        const int head = __shfl_sync(0xFFFFFFFFu, my_head, 8 * nt + g);
+        const uint16_t *src = p.q + tok * p.q_stride + static_cast<int64_t>(head) * D + t4 * (D / 4);
 #pragma unroll
-          for (int i = 0; i < KS / 2; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(src + 8 * i);
-            raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
-          }
-#pragma unroll
-          for (int i = 0; i < KS * 2; ++i) am = max(am, max((raw[i] << 16) & 0x7FFF0000u, raw[i] & 0x7FFF0000u));
-        } else {
-#pragma unroll
-          for (int i = 0; i < KS * 2; ++i) raw[i] = 0;
+        for (int i = 0; i < KS / 2; ++i) {
+          const uint4 v = rl > 0 ? *reinterpret_cast<const uint4 *>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+          qf[nt][2 * i][0] = v.x, qf[nt][2 * i][1] = v.y, qf[nt][2 * i + 1][0] = v.z, qf[nt][2 * i + 1][1] = v.w;
         }
+        lim[nt][0] = __shfl_sync(0xFFFFFFFFu, my_lim, 8 * nt + 2 * t4);
+        lim[nt][1] = __shfl_sync(0xFFFFFFFFu, my_lim, 8 * nt + 2 * t4 + 1);
+        least = min(least, min(lim[nt][0], lim[nt][1]));
+      }
+      if (first) fetch_first(w);
+      first = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint32_t am = 0;
+#pragma unroll
+        for (int i = 0; i < KS * 2; ++i)
+          am = max(am, max((qf[nt][i >> 1][i & 1] << 16) & 0x7FFF0000u, qf[nt][i >> 1][i & 1] & 0x7FFF0000u));
         am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
         am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
         // 2^sh brings the largest element to [2^14, 2^15) (bounded so that 2^sh and 2^-sh are normal)
@@ -331,20 +364,17 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 3 : 2) kv4_step_kernel(co
         const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
 #pragma unroll
         for (int i = 0; i < KS * 2; ++i) {
-          const float lo = __uint_as_float(raw[i] << 16) * up, hi = __uint_as_float(raw[i] & 0xFFFF0000u) * up;
-          qf[nt][i >> 1][i & 1] = pack_half2(lo, hi);
+          const uint32_t raw = qf[nt][i >> 1][i & 1];
+          qf[nt][i >> 1][i & 1] = pack_half2(__uint_as_float(raw << 16) * up, __uint_as_float(raw & 0xFFFF0000u) * up);
         }
         const float mine = p.softmax_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
         rs[nt][0] = __shfl_sync(0xFFFFFFFFu, mine, 8 * t4);      // lane 4 * (2 t4): column 2 t4
         rs[nt][1] = __shfl_sync(0xFFFFFFFFu, mine, 8 * t4 + 4);
-        lim[nt][0] = w.row_limit(8 * nt + 2 * t4);
-        lim[nt][1] = w.row_limit(8 * nt + 2 * t4 + 1);
-        least = min(least, min(lim[nt][0], lim[nt][1]));
       }
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
       if (tid < D / kKv4Block) S.nan_at[tid] = 0x7FFFFFFF;
-      named_bar_sync(1, 32 * kWarps);
+      __syncthreads();
 
       float o[KS][NT][4];
       float m[NT][2], l[NT][2];
@@ -355,22 +385,11 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 3 : 2) kv4_step_kernel(co
 #pragma unroll
         for (int i = 0; i < KS; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
       }
-      const int count = max(vis - w.tile, 0);
-      // stage i of the CTA goes to warp i % 4
-      for (int i = (warp - done % kWarps + kWarps) % kWarps; i < count; i += kWarps) {
-        const int st = done + i, slot = st % NS;
-        if (dead) break;
-        const bool ok = mbar_wait(&S.full[slot], (st / NS) & 1, &S.abort_flag);
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          dead = true;
-          break;
-        }
-        const typename Smem::Stage &T = S.stage[slot];
-        if (S.bad[slot]) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&S.empty[slot]);
-          continue;
-        }
+      for (int i = warp, h = NS; i < count; i += kWarps, h += 2) {
+        int slot = arrived();
+        if (slot < 0) break;
+        const bool bad = S.bad[warp][slot];
+        const typename Smem::Stage *T = &S.stage[warp][slot];
         const int key0 = (w.tile + i) * kTile;
         const bool edge = key0 + kTile > least;
         float s[MT][NT][4];
@@ -382,18 +401,24 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 3 : 2) kv4_step_kernel(co
           constexpr int W = D / 32;  // words of a lane's codes of one key
           uint32_t ca[W], cb[W];
           if constexpr (W == 4) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(T.k + ra * (D / 2) + t4 * 16);
-            const uint4 b = *reinterpret_cast<const uint4 *>(T.k + rb * (D / 2) + t4 * 16);
+            const uint4 a = *reinterpret_cast<const uint4 *>(T->c + ra * (D / 2) + t4 * 16);
+            const uint4 b = *reinterpret_cast<const uint4 *>(T->c + rb * (D / 2) + t4 * 16);
             ca[0] = a.x, ca[1] = a.y, ca[2] = a.z, ca[3] = a.w;
             cb[0] = b.x, cb[1] = b.y, cb[2] = b.z, cb[3] = b.w;
           } else {
-            const uint2 a = *reinterpret_cast<const uint2 *>(T.k + ra * (D / 2) + t4 * 8);
-            const uint2 b = *reinterpret_cast<const uint2 *>(T.k + rb * (D / 2) + t4 * 8);
+            const uint2 a = *reinterpret_cast<const uint2 *>(T->c + ra * (D / 2) + t4 * 8);
+            const uint2 b = *reinterpret_cast<const uint2 *>(T->c + rb * (D / 2) + t4 * 8);
             ca[0] = a.x, ca[1] = a.y;
             cb[0] = b.x, cb[1] = b.y;
           }
           const int blk = t4 * (D / 4) / kKv4Block;
-          const float fa = scale_value(T.ks[ra * (D / kKv4Block) + blk]), fb = scale_value(T.ks[rb * (D / kKv4Block) + blk]);
+          // 2^(byte - 127); a sum of them is infinite where a byte is 255 (NaN), which is looked at apart
+          float fa = __uint_as_float(static_cast<uint32_t>(T->s[ra * (D / kKv4Block) + blk]) << 23);
+          float fb = __uint_as_float(static_cast<uint32_t>(T->s[rb * (D / kKv4Block) + blk]) << 23);
+          if (fa + fb == INFINITY) {
+            if (fa == INFINITY) fa = __uint_as_float(0x7FC00000u);
+            if (fb == INFINITY) fb = __uint_as_float(0x7FC00000u);
+          }
           const uint32_t sa = pack_half2(fa, fa), sb = pack_half2(fb, fb);
 #pragma unroll
           for (int c = 0; c < W; ++c) {
@@ -409,8 +434,15 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 3 : 2) kv4_step_kernel(co
             }
           }
         }
+        __syncwarp();
+        fetch_half(w, count, h);
         // softmax: column c of tile nt is this lane's row pair; keys g and g + 8 of each 16
-        if (edge) {
+        if (bad) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = -INFINITY;
+        } else if (edge) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             const int ka = key0 + 16 * mt + key_of(g);
@@ -464,57 +496,70 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 3 : 2) kv4_step_kernel(co
             pb[mt][nt][1] = transpose8(pack_half2(p2, p3));
           }
         }
+        slot = arrived();
+        if (slot < 0) break;
+        T = &S.stage[warp][slot];
         // O^T += V^T P^T: a lane's channels are D/8 g .. + D/8 - 1, its keys 2 t4, 2 t4 + 1 and those + 8
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           const int kA = 16 * mt + key_of(2 * t4), kB = 16 * mt + key_of(2 * t4 + 1);
           constexpr int W = D / 64;
           uint32_t c4[4][W];
-          uint32_t sb[4];
+          float sf[4];
           const int blk = g * (D / 8) / kKv4Block;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int key = ((q & 1) ? kB : kA) + (q >> 1) * 8;
-            const uint8_t *src = T.v + key * (D / 2) + g * (D / 16);
+            const uint8_t *src = T->c + key * (D / 2) + g * (D / 16);
             if constexpr (W == 2) {
               const uint2 v = *reinterpret_cast<const uint2 *>(src);
               c4[q][0] = v.x, c4[q][1] = v.y;
             } else {
               c4[q][0] = *reinterpret_cast<const uint32_t *>(src);
             }
-            sb[q] = T.vs[key * (D / kKv4Block) + blk];
-            if (edge && key0 + key >= limit) sb[q] = 0;  // not a position of the unit: 2^-127, zero in fp16
+            sf[q] = __uint_as_float(static_cast<uint32_t>(T->s[key * (D / kKv4Block) + blk]) << 23);
           }
-          if (max(max(sb[0], sb[1]), max(sb[2], sb[3])) == 255u) {
+          if (edge || bad) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)  // not a position of the unit
+              if (bad || key0 + ((q & 1) ? kB : kA) + (q >> 1) * 8 >= limit) sf[q] = 0.f;
+          }
+          if ((sf[0] + sf[1]) + (sf[2] + sf[3]) == INFINITY) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              if (sb[q] == 255u) {
+              if (sf[q] == INFINITY) {
                 atomicMin(&S.nan_at[blk], key0 + ((q & 1) ? kB : kA) + (q >> 1) * 8);
-                sb[q] = 0;
+                sf[q] = 0.f;
               }
           }
-          const uint32_t sAB = pack_half2(scale_value(sb[0]), scale_value(sb[1]));
-          const uint32_t sCD = pack_half2(scale_value(sb[2]), scale_value(sb[3]));
+          const uint32_t sAB = pack_half2(sf[0], sf[1]), sCD = pack_half2(sf[2], sf[3]);
+          // Two keys' codes side by side in a byte before they are converted: 4 operations for 8 channels,
+          // half of what permuting the converted pairs takes.
 #pragma unroll
           for (int c = 0; c < W; ++c) {
-            uint32_t h[4][4];
+            uint32_t lo[2][4], hi[2][4];  // [keys A, B / C, D][channel pair]: even and odd channels
 #pragma unroll
-            for (int q = 0; q < 4; ++q) e2m1x8_to_half2(c4[q][c], h[q]);
+            for (int q = 0; q < 2; ++q) {
+              const uint32_t x = c4[2 * q][c], y = c4[2 * q + 1][c];
+              e2m1x8_to_half2((x & 0x0F0F0F0Fu) | (y << 4 & 0xF0F0F0F0u), lo[q]);
+              e2m1x8_to_half2((x >> 4 & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), hi[q]);
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint32_t a0 = hmul2(__byte_perm(h[0][k], h[1][k], 0x5410), sAB);
-              const uint32_t a1 = hmul2(__byte_perm(h[0][k], h[1][k], 0x7632), sAB);
-              const uint32_t a2 = hmul2(__byte_perm(h[2][k], h[3][k], 0x5410), sCD);
-              const uint32_t a3 = hmul2(__byte_perm(h[2][k], h[3][k], 0x7632), sCD);
+              const uint32_t a0 = hmul2(lo[0][k], sAB), a1 = hmul2(hi[0][k], sAB);
+              const uint32_t a2 = hmul2(lo[1][k], sCD), a3 = hmul2(hi[1][k], sCD);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma16816(o[4 * c + k][nt], a0, a1, a2, a3, pb[mt][nt][0], pb[mt][nt][1]);
             }
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.empty[slot]);
+        fetch_half(w, count, h + 1);
       }
-      done += count;
+      // the next unit's first copies are under way while this one is joined
+      Walk nx = w;
+      const bool more = nx.next();
+      if (more && !dead) fetch_first(nx);
 
       // ---- join the warps
 #pragma unroll
@@ -533,13 +578,13 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 3 : 2) kv4_step_kernel(co
           }
         }
       }
-      named_bar_sync(1, 32 * kWarps);
+      __syncthreads();
       const bool whole = w.tile == 0 && stop == w.tiles;
-      const int slot = 2 * static_cast<int>(blockIdx.x) + (w.tile == 0 ? 1 : 0);
+      const int part = 2 * static_cast<int>(blockIdx.x) + (w.tile == 0 ? 1 : 0);
       constexpr int V4 = D / 4;
       for (int e = tid; e < R * V4; e += 32 * kWarps) {
         const int r = e / V4, d = e % V4 * 4;
-        const int rl = w.row_limit(r);
+        const int rl = S.lim[r];
         if (rl == 0) continue;
         float mx = -INFINITY;
 #pragma unroll
@@ -557,18 +602,23 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 3 : 2) kv4_step_kernel(co
         }
         if (S.nan_at[d / kKv4Block] < rl) acc.x = acc.y = acc.z = acc.w = __uint_as_float(0x7FC00000u);
         if (whole) {
-          const int64_t row = w.row_index(r);
+          const int64_t row = S.index[r];
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
           const uint2 b = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
           *reinterpret_cast<uint2 *>(p.out + row * D + d) = b;
           if (d == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (mx - kPOff + log2f(sum)) * 0.6931471805599453f;
         } else {
-          *reinterpret_cast<float4 *>(P.part_o + (static_cast<int64_t>(slot) * R + r) * D + d) = acc;
-          if (d == 0) P.part_ml[slot * R + r] = make_float2(mx, sum);
+          *reinterpret_cast<float4 *>(P.part_o + (static_cast<int64_t>(part) * R + r) * D + d) = acc;
+          if (d == 0) P.part_ml[part * R + r] = make_float2(mx, sum);
         }
       }
-      named_bar_sync(1, 32 * kWarps);
-    } while (w.next());
+      __syncthreads();
+      if (!more) break;
+      w = nx;
+  }
+  if (dead) {  // let the copies in flight land before the CTA leaves
+    volatile int dummy = 0;
+    for (; used != issued; ++used) mbar_wait(&S.full[warp][used % NS], (used / NS) & 1, &dummy);
   }
   if (S.abort_flag && lane == 0) report(p.d_status, DSV4_DEV_TIMEOUT);
 }
@@ -580,37 +630,56 @@ template <int D>
 __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const __grid_constant__ AttnParams P, int R) {
   __shared__ int64_t prefix[kCombineThreads + 1], warp_sums[kCombineThreads / 32];
   const Kv4AttnLaunch &p = P.a;
-  pdl_wait();
-  pdl_launch_dependents();
-  const Line line{&p, p.Hq / p.Hk, R};
+  // (this grid starts once every CTA of the step kernel is past its own wait, so the lengths, which the
+  // step kernel does not write, can be read before this one's)
+  const Line line{&p, P.group, R, 31 - __clz(R)};
   const int chunk = (p.B + kCombineThreads - 1) / kCombineThreads;
   const int64_t all = line_prefix(line, kCombineThreads, chunk, prefix, warp_sums);
   const int ctas = slices(all, P.ctas);
   const int c = static_cast<int>(blockIdx.x) + 1;
-  if (c >= ctas) return;
   Walk w;
-  const int64_t from = slice_at(all, ctas, c);
-  w.begin(line, prefix, kCombineThreads, chunk, from, from + 1);
-  const int64_t unit = from - w.tile;
-  if (w.tile == 0 || slice_at(all, ctas, c - 1) > unit) return;
+  bool mine = c < ctas;
   int last = c;
-  while (last + 1 < ctas && slice_at(all, ctas, last + 1) < unit + w.tiles) ++last;
-  constexpr int V4 = D / 4;
+  if (mine) {
+    const int64_t from = slice_at(all, ctas, c);
+    w.begin(line, prefix, kCombineThreads, chunk, from, from + 1);
+    const int64_t unit = from - w.tile;
+    mine = w.tile != 0 && slice_at(all, ctas, c - 1) <= unit;
+    if (mine)
+      while (last + 1 < ctas && slice_at(all, ctas, last + 1) < unit + w.tiles) ++last;
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (!mine) return;
+  constexpr int V4 = D / 4, kAtOnce = 8;
   for (int e = threadIdx.x; e < R * V4; e += kCombineThreads) {
     const int r = e / V4, d = e % V4 * 4;
     if (w.row_limit(r) == 0) continue;
-    float mx = -INFINITY;
-    for (int k = c - 1; k <= last; ++k) mx = fmaxf(mx, P.part_ml[(2 * k + (k == c - 1)) * R + r].x);
+    float mx = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    for (int k = c - 1; k <= last; ++k) {
-      const int64_t slot = 2 * k + (k == c - 1);
-      const float2 ml = P.part_ml[slot * R + r];
-      const float4 v = *reinterpret_cast<const float4 *>(P.part_o + (slot * R + r) * D + d);
-      const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2_approx(ml.x - mx);
-      sum = fmaf(ml.y, f, sum);
-      acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
-      acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
+    for (int k0 = c - 1; k0 <= last; k0 += kAtOnce) {  // eight parts' loads at a time
+      float2 ml[kAtOnce];
+      float4 v[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int k = k0 + i;
+        const int64_t slot = 2 * k + (k == c - 1);
+        ml[i] = k <= last ? P.part_ml[slot * R + r] : make_float2(-INFINITY, 0.f);
+        v[i] = k <= last ? *reinterpret_cast<const float4 *>(P.part_o + (slot * R + r) * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float now = mx;
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) now = fmaxf(now, ml[i].x);
+      const float keep = mx == -INFINITY && sum == 0.f ? 0.f : ex2_approx(mx - now);
+      mx = now;
+      sum *= keep, acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const float f = ml[i].x == -INFINITY && ml[i].y == 0.f ? 0.f : ex2_approx(ml[i].x - mx);
+        sum = fmaf(ml[i].y, f, sum);
+        acc.x = fmaf(v[i].x, f, acc.x), acc.y = fmaf(v[i].y, f, acc.y);
+        acc.z = fmaf(v[i].z, f, acc.z), acc.w = fmaf(v[i].w, f, acc.w);
+      }
     }
     const int64_t row = w.row_index(r);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -623,9 +692,14 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const __gr
 // Whether the tensor-core form for 256-row blocks takes the call.
 bool prompt_rows(const Kv4AttnLaunch &p) { return static_cast<int64_t>(p.max_new) * (p.Hq / p.Hk) > 64; }
 
-// rows of a tile: one tile of 8 where the rows of a sequence fit, two otherwise
-int tile_rows(const Kv4AttnLaunch &p) { return static_cast<int64_t>(p.max_new) * (p.Hq / p.Hk) <= 8 ? 8 : 16; }
-int resident(int R) { return R == 8 ? 3 : 2; }
+// Rows of a tile: the smallest of 8, 16 and (64 channels) 32 that holds a sequence's rows in one. A tile of twice
+// the rows reads and converts each key once for both; at 128 channels the sums of 32 rows do not
+// fit the registers.
+int tile_rows(const Kv4AttnLaunch &p) {
+  const int64_t rows = static_cast<int64_t>(p.max_new) * (p.Hq / p.Hk);
+  return rows <= 8 ? 8 : (rows <= 16 || p.D == 128 ? 16 : 32);
+}
+int resident(const Kv4AttnLaunch &p) { return p.D * (tile_rows(p) / 8) <= 128 ? 3 : 2; }
 
 template <int D, int NT>
 cudaError_t launch_step(AttnParams &P, cudaStream_t st) {
@@ -641,7 +715,7 @@ cudaError_t launch_step(AttnParams &P, cudaStream_t st) {
 
 size_t kv4_attention_workspace_bytes(const Kv4AttnLaunch &p) {
   const int R = tile_rows(p);
-  const size_t rows = static_cast<size_t>(sm_count()) * resident(R) * 2 * R;
+  const size_t rows = static_cast<size_t>(sm_count()) * resident(p) * 2 * R;
   return align_up(rows * p.D * sizeof(float), 256) + align_up(rows * sizeof(float2), 256);
 }
 
@@ -650,11 +724,13 @@ cudaError_t launch_kv4_attention(const Kv4AttnLaunch &q, void *ws, cudaStream_t 
   AttnParams P{};
   P.a = q;
   const int R = tile_rows(q);
-  P.ctas = sm_count() * resident(R);
+  P.ctas = sm_count() * resident(q);
+  P.group = q.Hq / q.Hk;
   P.part_o = static_cast<float *>(ws);
   P.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(ws) +
                                          align_up(static_cast<size_t>(P.ctas) * 2 * R * q.D * sizeof(float), 256));
-  if (q.D == 64) return R == 8 ? launch_step<64, 1>(P, st) : launch_step<64, 2>(P, st);
+  if (q.D == 64)
+    return R == 8 ? launch_step<64, 1>(P, st) : (R == 16 ? launch_step<64, 2>(P, st) : launch_step<64, 4>(P, st));
   return R == 8 ? launch_step<128, 1>(P, st) : launch_step<128, 2>(P, st);
 }
 
