@@ -7,6 +7,7 @@ stream. It has no CPU fallback: without the built library every call raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 from dataclasses import dataclass, field
 
@@ -378,7 +379,9 @@ def sparse_mqa_decode(q, pos, cache: DeviceCache, ring: DeviceRing, *, q_dtype: 
 # the 4-bit key/value cache
 
 KV4_BLOCK = 32  # channels per scale byte
-_ROW_DT = {torch.float32: A.F32, torch.bfloat16: A.BF16}
+_U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
+_ROW_DT = {_F32: A.F32, _BF16: A.BF16}
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the handle alone: torch.cuda.current_stream() makes an object
 
 
 @dataclass
@@ -410,82 +413,82 @@ class DeviceKv4Cache:
         shape = kc.shape
         if len(shape) != 4 or shape[2] != A.PAGE_POSITIONS or vc.shape != shape:
             raise ValueError("codes are [num_pages, kv_heads, 256, dim/2], keys like values")
-        if ks.shape != vs.shape or ks.shape[:3] != shape[:3] or ks.shape[3] * KV4_BLOCK != shape[3] * 2:
+        pages, heads, rows, half = shape
+        if ks.shape != (pages, heads, rows, half * 2 // KV4_BLOCK) or vs.shape != ks.shape or half % (KV4_BLOCK // 2):
             raise ValueError("scales are [num_pages, kv_heads, 256, dim/32], keys like values")
+        dev = bt.get_device()
         for t in (kc, vc, ks, vs):
-            if t.dtype != torch.uint8 or not t.is_contiguous() or t.device != bt.device:
+            if t.dtype is not _U8 or not t.is_contiguous() or t.get_device() != dev:
                 raise ValueError("codes and scales are contiguous uint8 tensors on the table's device")
-        if bt.dtype != torch.int32 or bt.dim() != 2 or not bt.is_contiguous():
+        if bt.dtype is not _I32 or bt.dim() != 2 or not bt.is_contiguous():
             raise ValueError("block_table is a contiguous [B, max_blocks] int32 tensor")
-        return A.Kv4Cache(_ptr(kc), _ptr(vc), _ptr(ks), _ptr(vs), _ptr(bt), shape[0], bt.shape[1], shape[1],
-                          shape[3] * 2)
+        return A.Kv4Cache(_ptr(kc), _ptr(vc), _ptr(ks), _ptr(vs), _ptr(bt), pages, bt.shape[1], heads, half * 2)
 
 
-def _rows(name: str, t, heads: int | None = None, dim: int | None = None):
-    """(pointer, elements between tokens) of new tokens' rows [T, heads, dim]; the token axis may be strided."""
-    if t.dim() != 3 or t.dtype not in _ROW_DT:
-        raise ValueError(f"{name} is a [T, heads, dim] float32 or bfloat16 tensor")
+# The calls below may be a decode step's, a few microseconds of device time each, so they are written for little
+# time on the host: cheap attribute checks, no context manager where the tensors' device is the current one.
+
+def _elsewhere(device: int, stream) -> contextlib.ExitStack | None:
+    """None where the call can be made as it is: on the current stream of the current device, which is
+    the tensors'. Otherwise a context that makes it so (outputs are then allocated there too)."""
+    if stream is None and (device < 0 or device == torch.cuda.current_device()):
+        return None
+    ctx = contextlib.ExitStack()
+    if device >= 0:
+        ctx.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        ctx.enter_context(torch.cuda.stream(stream))
+    return ctx
+
+
+def _rows(name: str, t, device: int, dtype, heads: int = 0, dim: int = 0):
+    """(pointer, heads, elements between tokens) of new tokens' rows [T, heads, dim]; the token axis may be strided."""
+    if t.dim() != 3 or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{name} is a [T, heads, dim] {dtype} tensor on the call's device")
     T, H, D = t.shape
-    if (heads is not None and H != heads) or (dim is not None and D != dim):
-        raise ValueError(f"{name} has {H} heads of {D}, expected {heads} of {dim}")
+    if (heads and H != heads) or (dim and D != dim):
+        raise ValueError(f"{name} has {H} heads of {D}, expected {heads or 'any'} of {dim}")
     st, sh, sd = t.stride()
-    if sd != 1 or (H > 1 and sh != D):
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{name}: the heads of a token are contiguous rows")
-    return _ptr(t), (st if T > 1 else H * D)
+    return _ptr(t), H, (st if T > 1 else H * D)
 
 
-def _lengths(cu_seqlens, start_pos, T_device):
-    if cu_seqlens.dtype != torch.int32 or start_pos.dtype != torch.int32:
-        raise ValueError("cu_seqlens and start_pos are int32 tensors")
-    if cu_seqlens.dim() != 1 or start_pos.dim() != 1 or cu_seqlens.shape[0] != start_pos.shape[0] + 1:
-        raise ValueError("cu_seqlens is [B + 1], start_pos [B]")
-    if not (cu_seqlens.is_contiguous() and start_pos.is_contiguous()):
-        raise ValueError("cu_seqlens and start_pos are contiguous")
-    if cu_seqlens.device != T_device or start_pos.device != T_device:
+def _lengths(cu_seqlens, start_pos, device: int) -> int:
+    if cu_seqlens.dtype is not _I32 or start_pos.dtype is not _I32 or cu_seqlens.dim() != 1 or start_pos.dim() != 1:
+        raise ValueError("cu_seqlens [B + 1] and start_pos [B] are int32 tensors")
+    B = start_pos.shape[0]
+    if cu_seqlens.shape[0] != B + 1 or not (cu_seqlens.is_contiguous() and start_pos.is_contiguous()):
+        raise ValueError("cu_seqlens is [B + 1] and start_pos [B], contiguous")
+    if cu_seqlens.get_device() != device or start_pos.get_device() != device:
         raise ValueError("all tensors of a call are on one device")
-    return start_pos.shape[0]
+    return B
 
 
-def _dense_out(name, t, shape, dtypes, device):
-    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} is a contiguous {tuple(shape)} tensor on the inputs' device")
+def _out(name, t, like, dtype):
+    """A dense tensor of like's shape: new, or the caller's after a check."""
+    if t is None:
+        return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
+    if t.shape != like.shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != like.get_device():
+        raise ValueError(f"{name} is a contiguous {tuple(like.shape)} {dtype} tensor on the inputs' device")
     return t
 
 
-def _gamma(name, g, dim, device):
-    if g is None:
+def _opt(name, t, dtype, shape, device: int):
+    """Pointer of an optional dense tensor of this shape."""
+    if t is None:
         return None
-    if g.dtype != torch.float32 or tuple(g.shape) != (dim,) or not g.is_contiguous() or g.device != device:
-        raise ValueError(f"{name} is a contiguous float32 [{dim}] tensor")
-    return g.data_ptr()
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name} is a contiguous {tuple(shape)} {dtype} tensor on the inputs' device")
+    return _ptr(t)
 
 
-def _status_word(d_status, device):
-    if d_status is None:
+def _status(t, device: int):
+    if t is None:
         return None
-    if d_status.dtype != torch.int32 or d_status.numel() < 1 or d_status.device != device:
+    if t.dtype is not _I32 or t.numel() < 1 or t.get_device() != device:
         raise ValueError("d_status is an int32 tensor on the inputs' device")
-    return d_status.data_ptr()
-
-
-class _On:
-    """The device of a call's tensors made current, and its stream (outputs are allocated there)."""
-
-    def __init__(self, device, stream):
-        self.ctx = []
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.ctx.append(torch.cuda.device(device))
-        if stream is not None:
-            self.ctx.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        for c in reversed(self.ctx):
-            c.__exit__(*exc)
+    return _ptr(t)
 
 
 def qk_norm_rope(q, k, cu_seqlens, start_pos, *, gamma_q=None, gamma_k=None, eps: float = 1e-6, rope_dims: int = 64,
@@ -496,30 +499,36 @@ def qk_norm_rope(q, k, cu_seqlens, start_pos, *, gamma_q=None, gamma_k=None, eps
     some = q if q is not None else k
     if some is None:
         raise ValueError("qk_norm_rope needs q or k")
-    dev, T, D = some.device, some.shape[0], some.shape[2]
-    if q is not None and k is not None and (k.dtype != q.dtype or k.device != dev or k.shape[0] != T):
-        raise ValueError("q and k have one dtype, device and number of tokens")
+    dev = some.get_device()
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return qk_norm_rope(q, k, cu_seqlens, start_pos, gamma_q=gamma_q, gamma_k=gamma_k, eps=eps,
+                                rope_dims=rope_dims, rope_base=rope_base, out_dtype=out_dtype, q_out=q_out, k_out=k_out,
+                                d_status=d_status)
+    dt = some.dtype
+    if dt not in _ROW_DT:
+        raise ValueError("q and k are float32 or bfloat16")
+    T, _, D = some.shape if some.dim() == 3 else (0, 0, 0)
     B = _lengths(cu_seqlens, start_pos, dev)
-    out_dtype = out_dtype or some.dtype
-    with _On(dev, stream) as st:
-        ptrs, outs, heads = [], [], []
-        for name, t, o in (("q", q, q_out), ("k", k, k_out)):
-            if t is None:
-                ptrs.append((None, 0))
-                outs.append(None)
-                heads.append(0)
-                continue
-            ptrs.append(_rows(name, t, dim=D))
-            outs.append(torch.empty(t.shape, dtype=out_dtype, device=dev) if o is None else
-                        _dense_out(name + "_out", o, t.shape, (out_dtype,), dev))
-            heads.append(t.shape[1])
-        a = A.QkNormRopeArgs(B, T, heads[0], heads[1], D, ptrs[0][0], ptrs[1][0], ptrs[0][1], ptrs[1][1],
-                             _ROW_DT[some.dtype], _ROW_DT.get(out_dtype, -1), _gamma("gamma_q", gamma_q, D, dev),
-                             _gamma("gamma_k", gamma_k, D, dev), eps, A.Rope(rope_dims, rope_base),
-                             cu_seqlens.data_ptr(), start_pos.data_ptr(), _ptr(outs[0]), _ptr(outs[1]),
-                             _status_word(d_status, dev))
-        A.check("dsv4_qk_norm_rope", A.load().dsv4_qk_norm_rope(C.byref(a), st))
-    return outs[0], outs[1]
+    out_dtype = out_dtype or dt
+    qp = kp = qo = ko = None
+    qh = kh = qs = ks = 0
+    if q is not None:
+        qp, qh, qs = _rows("q", q, dev, dt, 0, D)
+        q_out = _out("q_out", q_out, q, out_dtype)
+        qo = q_out.data_ptr()
+    if k is not None:
+        kp, kh, ks = _rows("k", k, dev, dt, 0, D)
+        if k.shape[0] != T:
+            raise ValueError("q and k have one number of tokens")
+        k_out = _out("k_out", k_out, k, out_dtype)
+        ko = k_out.data_ptr()
+    a = A.QkNormRopeArgs(B, T, qh, kh, D, qp, kp, qs, ks, _ROW_DT[dt], _ROW_DT.get(out_dtype, -1),
+                         _opt("gamma_q", gamma_q, _F32, (D,), dev), _opt("gamma_k", gamma_k, _F32, (D,), dev), eps,
+                         (rope_dims, rope_base), _ptr(cu_seqlens), _ptr(start_pos), qo, ko, _status(d_status, dev))
+    A.check("dsv4_qk_norm_rope", A.load().dsv4_qk_norm_rope(C.byref(a), _raw_stream(dev)))
+    return (q_out if q is not None else None), (k_out if k is not None else None)
 
 
 def kv4_append(k, v, cu_seqlens, start_pos, cache: DeviceKv4Cache, *, gamma_k=None, eps: float = 1e-6,
@@ -529,57 +538,65 @@ def kv4_append(k, v, cu_seqlens, start_pos, cache: DeviceKv4Cache, *, gamma_k=No
     [T, Hq, D], if given, normed and rotated in the same launch (bfloat16, unless q_out says
     otherwise). Returns (q_out, k_stored, v_stored): None without q; the stored rows' values
     (bfloat16, exact) with with_stored, else None."""
-    dev, T = k.device, k.shape[0]
+    dev = k.get_device()
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return kv4_append(k, v, cu_seqlens, start_pos, cache, gamma_k=gamma_k, eps=eps, rope_dims=rope_dims,
+                              rope_base=rope_base, q=q, gamma_q=gamma_q, q_out=q_out, with_stored=with_stored,
+                              k_stored=k_stored, v_stored=v_stored, d_status=d_status)
+    dt = k.dtype
+    if dt not in _ROW_DT:
+        raise ValueError("k, v and q are float32 or bfloat16")
     B = _lengths(cu_seqlens, start_pos, dev)
     cs = cache.struct()
-    if cache.block_table.shape[0] != B or cache.block_table.device != dev:
-        raise ValueError("the cache's table has one row per sequence, on the inputs' device")
-    if v.dtype != k.dtype or v.device != dev or v.shape != k.shape:
-        raise ValueError("k and v have one shape, dtype and device")
-    if q is not None and (q.dtype != k.dtype or q.device != dev or q.shape[0] != T):
-        raise ValueError("q has k's dtype, device and number of tokens")
-    kp, ks = _rows("k", k, cs.kv_heads, cs.dim)
-    vp, vs = _rows("v", v, cs.kv_heads, cs.dim)
-    with _On(dev, stream) as st:
-        qp, qs, qh, qdt = None, 0, 0, A.BF16
-        if q is not None:
-            qp, qs = _rows("q", q, dim=cs.dim)
-            qh = q.shape[1]
-            if q_out is None:
-                q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-            qdt = _ROW_DT[_dense_out("q_out", q_out, q.shape, tuple(_ROW_DT), dev).dtype]
-        elif q_out is not None:
-            raise ValueError("q_out needs q")
-        if with_stored:
-            k_stored = torch.empty(k.shape, dtype=torch.bfloat16, device=dev) if k_stored is None else k_stored
-            v_stored = torch.empty(k.shape, dtype=torch.bfloat16, device=dev) if v_stored is None else v_stored
-        for name, t in (("k_stored", k_stored), ("v_stored", v_stored)):
-            if t is not None:
-                _dense_out(name, t, k.shape, (torch.bfloat16,), dev)
-        a = A.Kv4AppendArgs(B, T, kp, vp, ks, vs, _ROW_DT[k.dtype], _gamma("gamma_k", gamma_k, cs.dim, dev), eps,
-                            A.Rope(rope_dims, rope_base), cu_seqlens.data_ptr(), start_pos.data_ptr(), cs, qh, qp, qs,
-                            _gamma("gamma_q", gamma_q, cs.dim, dev), _ptr(q_out), qdt, _ptr(k_stored), _ptr(v_stored),
-                            _status_word(d_status, dev))
-        A.check("dsv4_kv4_append", A.load().dsv4_kv4_append(C.byref(a), st))
+    _table_of(cache, B, dev)
+    D = cs.dim
+    kp, _, ks = _rows("k", k, dev, dt, cs.kv_heads, D)
+    vp, _, vs = _rows("v", v, dev, dt, cs.kv_heads, D)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError("k and v have one number of tokens")
+    qp = qo = None
+    qh = qs = 0
+    qdt = A.BF16
+    if q is not None:
+        qp, qh, qs = _rows("q", q, dev, dt, 0, D)
+        if q.shape[0] != T:
+            raise ValueError("q and k have one number of tokens")
+        q_out = _out("q_out", q_out, q, _BF16 if q_out is None or q_out.dtype is not _F32 else _F32)
+        qdt = _ROW_DT[q_out.dtype]
+        qo = q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if with_stored or k_stored is not None:
+        k_stored = _out("k_stored", k_stored, k, _BF16)
+    if with_stored or v_stored is not None:
+        v_stored = _out("v_stored", v_stored, v, _BF16)
+    a = A.Kv4AppendArgs(B, T, kp, vp, ks, vs, _ROW_DT[dt], _opt("gamma_k", gamma_k, _F32, (D,), dev), eps,
+                        (rope_dims, rope_base), _ptr(cu_seqlens), _ptr(start_pos), cs, qh, qp, qs,
+                        _opt("gamma_q", gamma_q, _F32, (D,), dev), qo, qdt, _ptr(k_stored), _ptr(v_stored),
+                        _status(d_status, dev))
+    A.check("dsv4_kv4_append", A.load().dsv4_kv4_append(C.byref(a), _raw_stream(dev)))
     return q_out, k_stored, v_stored
+
+
+def _table_of(cache, B: int, device: int):
+    bt = cache.block_table
+    if bt.shape[0] != B or bt.get_device() != device:
+        raise ValueError("the cache's table has one row per sequence, on the inputs' device")
 
 
 def kv4_attention_args(q, cu_seqlens, start_pos, cache: DeviceKv4Cache, *, max_new: int, softmax_scale: float = 0.0,
                        out=None, lse=None, d_status=None) -> A.Kv4AttentionArgs:
-    dev = q.device
+    dev = q.get_device()
     B = _lengths(cu_seqlens, start_pos, dev)
     cs = cache.struct()
-    if cache.block_table.shape[0] != B or cache.block_table.device != dev:
-        raise ValueError("the cache's table has one row per sequence, on the inputs' device")
-    if q.dtype != torch.bfloat16:
-        raise ValueError("q is bfloat16")
-    qp, qs = _rows("q", q, dim=cs.dim)
-    if out is not None:
-        _dense_out("out", out, q.shape, (torch.bfloat16,), dev)
-    if lse is not None:
-        _dense_out("lse", lse, q.shape[:2], (torch.float32,), dev)
-    return A.Kv4AttentionArgs(B, q.shape[0], max_new, q.shape[1], cs.dim, qp, qs, cu_seqlens.data_ptr(),
-                              start_pos.data_ptr(), cs, softmax_scale, _ptr(out), _ptr(lse), _status_word(d_status, dev))
+    _table_of(cache, B, dev)
+    qp, qh, qs = _rows("q", q, dev, _BF16, 0, cs.dim)
+    return A.Kv4AttentionArgs(B, q.shape[0], max_new, qh, cs.dim, qp, qs, _ptr(cu_seqlens), _ptr(start_pos), cs,
+                              softmax_scale, _opt("out", out, _BF16, q.shape, dev),
+                              _opt("lse", lse, _F32, q.shape[:2], dev), _status(d_status, dev))
 
 
 def kv4_attention_workspace_size(args: A.Kv4AttentionArgs) -> int:
@@ -589,7 +606,7 @@ def kv4_attention_workspace_size(args: A.Kv4AttentionArgs) -> int:
 
 def kv4_attention_workspace(q, cu_seqlens, cache: DeviceKv4Cache, *, max_new: int) -> torch.Tensor:
     """A workspace for kv4_attention calls of these sizes (one call at a time may use it)."""
-    with _On(q.device, None):
+    with _elsewhere(q.get_device(), None) or contextlib.nullcontext():
         n = kv4_attention_workspace_size(kv4_attention_args(q, cu_seqlens, cu_seqlens[:-1], cache, max_new=max_new))
         if n == 0:
             A.check("dsv4_kv4_attention_workspace_size", A.ERR_INVALID_ARG)
@@ -600,20 +617,24 @@ def kv4_attention(q, cu_seqlens, start_pos, cache: DeviceKv4Cache, *, max_new: i
                   with_lse: bool = False, out=None, lse=None, d_status=None, workspace=None, stream=None):
     """Causal attention of the new tokens q [T, Hq, D] bfloat16 (normed and rotated) over the 4-bit
     cache that holds their keys and values already. Returns out, or (out, lse) with with_lse."""
-    dev = q.device
-    with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-        if with_lse and lse is None:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
-        a = kv4_attention_args(q, cu_seqlens, start_pos, cache, max_new=max_new, softmax_scale=softmax_scale, out=out,
-                               lse=lse, d_status=d_status)
-        if workspace is None:
-            workspace = torch.empty(max(kv4_attention_workspace_size(a), 256), dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace is a contiguous tensor on the inputs' device")
-        A.check("dsv4_kv4_attention", A.load().dsv4_kv4_attention(
-            C.byref(a), workspace.data_ptr(), workspace.numel() * workspace.element_size(), st))
+    dev = q.get_device()
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return kv4_attention(q, cu_seqlens, start_pos, cache, max_new=max_new, softmax_scale=softmax_scale,
+                                 with_lse=with_lse, out=out, lse=lse, d_status=d_status, workspace=workspace)
+    if out is None:
+        out = _out("out", None, q, _BF16)
+    if with_lse and lse is None:
+        lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
+    a = kv4_attention_args(q, cu_seqlens, start_pos, cache, max_new=max_new, softmax_scale=softmax_scale, out=out,
+                           lse=lse, d_status=d_status)
+    if workspace is None:
+        workspace = torch.empty(max(kv4_attention_workspace_size(a), 256), dtype=_U8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace is a contiguous tensor on the inputs' device")
+    A.check("dsv4_kv4_attention", A.load().dsv4_kv4_attention(
+        C.byref(a), _ptr(workspace), workspace.numel() * workspace.element_size(), _raw_stream(dev)))
     return (out, lse) if with_lse else out
 
 
