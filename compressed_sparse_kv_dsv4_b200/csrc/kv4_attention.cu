@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kThreadsA, StepShape<D, NT>::kResident)
         if (whole) {
           const int64_t row = S.index[r];
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          const uint2 b = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          const uint2 b = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
           *reinterpret_cast<uint2 *>(p.out + row * D + d) = b;
           if (d == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (mx - kPOff + log2f(sum)) * 0.6931471805599453f;
         } else {
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const __gr
     const int64_t row = w.row_index(r);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     *reinterpret_cast<uint2 *>(p.out + row * D + d) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     if (d == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (mx - kPOff + log2f(sum)) * 0.6931471805599453f;
   }
 }

@@ -20,6 +20,8 @@
 // part is kept in the textbook's order: squares rounded, then summed (four neighbours in turn at 128
 // channels, channels 32 apart at 64; then halves onto halves), x * (1 / rms) * gamma, products of the
 // rotation rounded before their difference; angle, sine and cosine in float64.
+#include <type_traits>
+
 #include "kv4_device.cuh"
 
 namespace dsv4 {
@@ -35,32 +37,37 @@ struct HeadsParams {
   int row_split;   // blocks along y, each on every row_split-th group of rows
   int tok_blocks;  // blocks along x
   int step;        // tokens of a block's step
-  uint32_t div_q, div_k;  // ceil(2^32 / Hq), ceil(2^32 / Hk): row numbers (below 2^17) over heads (up to 2^14)
 };
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// a lane's E values of a row as they lie in memory, and as floats
 template <int E, bool F32>
-__device__ __forceinline__ void load_vals(const void *base, int64_t off, float (&x)[E]) {
-  if constexpr (F32) {
-    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + off);
+struct Raw {
+  static constexpr int kWords = F32 ? E / 4 : E / 8;  // 16 bytes each
+  uint4 w[kWords];
+  __device__ __forceinline__ void load(const void *base, int64_t off) {
+    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(base) + off * (F32 ? 4 : 2));
 #pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      const float4 v = __ldcs(p + i);
-      x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-    }
-  } else {
-    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + off);
+    for (int i = 0; i < kWords; ++i) w[i] = __ldcs(p + i);
+  }
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < E / 8; ++i) {
-      const uint4 v = __ldcs(p + i);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int i = 0; i < kWords; ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void values(float (&x)[E]) const {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[8 * i + 2 * k] = bf16_lo(w[k]), x[8 * i + 2 * k + 1] = bf16_hi(w[k]);
+    for (int i = 0; i < kWords; ++i) {
+      const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (F32) x[4 * i + k] = __uint_as_float(v[k]);
+        else x[8 * i + 2 * k] = bf16_lo(v[k]), x[8 * i + 2 * k + 1] = bf16_hi(v[k]);
+      }
     }
   }
-}
+};
 
 template <int E>
 __device__ __forceinline__ void store_vals(void *base, dsv4_dtype dt, int64_t off, const float (&x)[E]) {
@@ -72,8 +79,8 @@ __device__ __forceinline__ void store_vals(void *base, dsv4_dtype dt, int64_t of
     uint4 *p = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + off);
 #pragma unroll
     for (int i = 0; i < E / 8; ++i)
-      p[i] = make_uint4(pack_bf16x2(x[8 * i], x[8 * i + 1]), pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
-                        pack_bf16x2(x[8 * i + 4], x[8 * i + 5]), pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
+      p[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                        pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
   }
 }
 
@@ -149,6 +156,59 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
+// Sine and cosine of `a` (finite, |a| below 2^31), to about 1e-11 absolute, rounded once to float32: the nearest
+// multiple k of pi/2 is taken off with two constants (pi/2 to 107 bits), the rest, within pi/4, goes into
+// the Taylor polynomials up to r^11 and r^12 (next terms 7e-12 and 4e-13), and k's low bits turn the quadrant. The
+// library's float64 sincos took the step of one token from 4.4 to 15 us where few pairs are worked out per block.
+__device__ __forceinline__ float2 cos_sin(double a) {
+  constexpr double kHi = 1.5707963267948966, kLo = 6.123233995736766e-17, kInv = 0.6366197723675814;
+  const double k = rint(a * kInv);
+  const double r = fma(-k, kLo, fma(-k, kHi, a)), q = r * r;
+  double s = fma(q, -1.0 / 39916800.0, 1.0 / 362880.0);
+  s = fma(s, q, -1.0 / 5040.0);
+  s = fma(s, q, 1.0 / 120.0);
+  s = fma(s, q, -1.0 / 6.0);
+  s = fma(s * q, r, r);
+  double c = fma(q, 1.0 / 479001600.0, -1.0 / 3628800.0);
+  c = fma(c, q, 1.0 / 40320.0);
+  c = fma(c, q, -1.0 / 720.0);
+  c = fma(c, q, 1.0 / 24.0);
+  c = fma(c, q, -0.5);
+  c = fma(c, q, 1.0);
+  const int n = static_cast<int>(static_cast<int64_t>(k)) & 3;
+  const float fs = static_cast<float>(s), fc = static_cast<float>(c);
+  const float x = (n & 1) ? fs : fc, y = (n & 1) ? fc : fs;
+  return make_float2(n == 1 || n == 2 ? -x : x, n >= 2 ? -y : y);
+}
+
+enum { kQuery, kKey, kValue };
+
+// A thread's rows of one kind in a step: row number it = first, first + S, ... below total, which is head it % H of
+// token it / H. Divisions only at the start: the walk adds S = dj * H + dh.
+struct RowWalk {
+  int j, h, left;      // token of the step, head, rows still to come (this one included)
+  int64_t in, out;     // element offsets of the row from the step's first token in the input and the dense output
+  __device__ __forceinline__ void begin(int first, int S, int H, int total, int64_t stride, int D) {
+    left = first < total ? (total - first + S - 1) / S : 0;
+    j = first / H;
+    h = first - j * H;
+    in = j * stride + h * D;
+    out = static_cast<int64_t>(first) * D;
+  }
+  __device__ __forceinline__ void next(int S, int dj, int dh, int H, int64_t stride, int D) {
+    --left;
+    j += dj;
+    h += dh;
+    in += dj * stride + dh * D;
+    out += static_cast<int64_t>(S) * D;
+    if (h >= H) {
+      h -= H;
+      ++j;
+      in += stride - H * D;
+    }
+  }
+};
+
 template <int D, bool F32>
 __global__ void __launch_bounds__(kHThreads, D <= 256 ? 4 : 3) kv4_heads_kernel(const __grid_constant__ HeadsParams P) {
   constexpr int E = D <= 256 ? 8 : D / 32;  // values of a row per lane
@@ -157,204 +217,209 @@ __global__ void __launch_bounds__(kHThreads, D <= 256 ? 4 : 3) kv4_heads_kernel(
   const Kv4HeadsLaunch &p = P.a;
   __shared__ __align__(16) float2 turn[kHTokens][kHPairs];  // cos and sin of a token's pairs
   __shared__ __align__(16) float gamma[2][D];               // of queries and of keys
-  __shared__ int first_sh;
   __shared__ int64_t pos_sh[kHTokens], cell_sh[kHTokens];  // position (-1: no such token), page * 256 + row (-1: none)
   const int tid = threadIdx.x, l = tid % L, g = tid / L;
   const bool cached = p.cache.k_codes != nullptr;
   const int pairs = p.rope_dims / 2, rope_at = D - p.rope_dims;
+  const bool aligned = rope_at % 8 == 0;  // a lane's pairs are all turned or none, and start at a multiple of four
   pdl_wait();
   pdl_launch_dependents();
   for (int i = tid; i < 2 * D; i += kHThreads) {
     const float *src = i < D ? p.gamma_q : p.gamma_k;
     gamma[i / D][i % D] = src ? src[i % D] : 1.f;
   }
+  const int first = static_cast<int>(blockIdx.y) * G + g, S = P.row_split * G;
+  const int djq = p.Hq ? S / p.Hq : 0, dhq = S - djq * p.Hq, djk = p.Hk ? S / p.Hk : 0, dhk = S - djk * p.Hk;
 
-  // Row number -> the row: query rows of the step's tokens first, then keys, then values.
-  struct Row {
-    int kind, j, h;  // 0 query, 1 key, 2 value (3: none); token of the step; head
-  };
-  auto row_of = [&](int it, int nt) {
-    Row r;
-    const int nq = nt * p.Hq, nk = nt * p.Hk;
-    r.kind = it < nq ? 0 : (it < nq + nk ? 1 : (cached && it < nq + 2 * nk ? 2 : 3));
-    const uint32_t at = r.kind == 0 ? it : (r.kind == 1 ? it - nq : (r.kind == 2 ? it - nq - nk : 0));
-    r.j = r.kind == 3 ? 0 : static_cast<int>(r.kind == 0 ? __umulhi(at, P.div_q) : __umulhi(at, P.div_k));
-    if ((r.kind == 0 ? p.Hq : p.Hk) == 1) r.j = static_cast<int>(at);  // (2^32 / 1 does not fit)
-    r.h = static_cast<int>(at) - r.j * (r.kind == 0 ? p.Hq : p.Hk);
-    return r;
-  };
-  auto load_row = [&](const Row &r, int64_t t0, float(&x)[E]) {
-    if (r.kind == 3) {
-#pragma unroll
-      for (int i = 0; i < E; ++i) x[i] = 0.f;
-      return;
-    }
-    const void *src = r.kind == 0 ? p.q : (r.kind == 1 ? p.k : p.v);
-    const int64_t stride = r.kind == 0 ? p.q_stride : (r.kind == 1 ? p.k_stride : p.v_stride);
-    load_vals<E, F32>(src, (t0 + r.j) * stride + r.h * D + l * E, x);
-  };
-  auto finish_row = [&](const Row &r, int64_t t0, float(&x)[E]) {
-    const float sum = sum_squares<D, E>(x);
-    const bool live = r.kind < 3 && pos_sh[r.j] >= 0 && (r.kind == 0 || !cached || cell_sh[r.j] >= 0);
-    const int64_t t = t0 + r.j;
-    if (r.kind < 2) {
-      if (r.kind == 0 ? p.gamma_q != nullptr : p.gamma_k != nullptr) {
-        const float inv = rsqrtf(__fadd_rn(sum * (1.f / D), p.eps));
-        const float4 *gm = reinterpret_cast<const float4 *>(&gamma[r.kind][l * E]);
+  using Row = Raw<E, F32>;
+  // one row: x in, results out
+  auto finish = [&](auto kind_tag, const Row &raw, const RowWalk &w, bool in, int64_t t0) {
+    constexpr int kKind = decltype(kind_tag)::value;
+    float x[E];
+    raw.values(x);
+    bool live = in && pos_sh[w.j] >= 0;
+    if (kKind != kQuery && cached) live = live && cell_sh[w.j] >= 0;
+    if constexpr (kKind != kValue) {
+      if ((kKind == kQuery ? p.gamma_q : p.gamma_k) != nullptr) {
+        const float inv = rsqrtf(__fadd_rn(sum_squares<D, E>(x) * (1.f / D), p.eps));
+        const float4 *gm = reinterpret_cast<const float4 *>(&gamma[kKind][l * E]);
 #pragma unroll
         for (int i = 0; i < E / 4; ++i) {
-          const float4 w = gm[i];
-          x[4 * i] = __fmul_rn(__fmul_rn(x[4 * i], inv), w.x);
-          x[4 * i + 1] = __fmul_rn(__fmul_rn(x[4 * i + 1], inv), w.y);
-          x[4 * i + 2] = __fmul_rn(__fmul_rn(x[4 * i + 2], inv), w.z);
-          x[4 * i + 3] = __fmul_rn(__fmul_rn(x[4 * i + 3], inv), w.w);
+          const float4 m = gm[i];
+          x[4 * i] = __fmul_rn(__fmul_rn(x[4 * i], inv), m.x);
+          x[4 * i + 1] = __fmul_rn(__fmul_rn(x[4 * i + 1], inv), m.y);
+          x[4 * i + 2] = __fmul_rn(__fmul_rn(x[4 * i + 2], inv), m.z);
+          x[4 * i + 3] = __fmul_rn(__fmul_rn(x[4 * i + 3], inv), m.w);
         }
       }
+      auto rotate = [&](int i, float c, float s) {
+        const float a = x[i], b = x[i + 1];
+        x[i] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+        x[i + 1] = __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
+      };
+      const int d0 = l * E - rope_at;  // even: rope_dims, D and E are
+      if (aligned) {
+        if (d0 + E > 0) {
+          const float4 *cs = reinterpret_cast<const float4 *>(&turn[w.j][0]) + d0 / 4;
 #pragma unroll
-      for (int i = 0; i < E; i += 2) {
-        const int d = l * E + i - rope_at;  // even: rope_dims, D and E are
-        if (d >= 0) {
-          const float2 cs = turn[r.j][d >> 1];
-          const float a = x[i], b = x[i + 1];
-          x[i] = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
-          x[i + 1] = __fadd_rn(__fmul_rn(a, cs.y), __fmul_rn(b, cs.x));
+          for (int i = 0; i < E; i += 4) {
+            if (E > 8 && d0 + i < 0) continue;  // (16 values of a lane, 8 of them turned)
+            const float4 v = cs[i / 4];
+            rotate(i, v.x, v.y);
+            rotate(i + 2, v.z, v.w);
+          }
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; i += 2)
+          if (d0 + i >= 0) rotate(i, turn[w.j][(d0 + i) >> 1].x, turn[w.j][(d0 + i) >> 1].y);
       }
-      if (r.kind == 0 || !cached) {
-        if (live) {
-          const int64_t off = (t * (r.kind == 0 ? p.Hq : p.Hk) + r.h) * D + l * E;
-          store_vals<E>(r.kind == 0 ? p.q_out : p.k_out, p.out_dt, off, x);
+      if (kKind == kQuery || !cached) {
+        const int64_t off = t0 * (kKind == kQuery ? p.Hq : p.Hk) * D + w.out + l * E;
+        if (live) store_vals<E>(kKind == kQuery ? p.q_out : p.k_out, p.out_dt, off, x);
+        return;
+      }
+    }
+    if constexpr (D <= 128 && kKind != kQuery) {
+      float am = fabsf(x[0]);
+#pragma unroll
+      for (int i = 1; i < E; ++i) am = max_nan(am, fabsf(x[i]));
+      am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+      am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+      if (live) {
+        const int sb = block_scale(am);
+        const float up = __uint_as_float(static_cast<uint32_t>(sb == 255 ? 0 : 254 - sb) << 23);  // 2^-k
+        uint32_t c = 0;
+        if (sb != 255) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) c |= e2m1_pair(x[2 * i] * up, x[2 * i + 1] * up) << (8 * i);
+        }
+        const int64_t cell = cell_sh[w.j];
+        const int64_t row = (cell / DSV4_PAGE_POSITIONS * p.Hk + w.h) * DSV4_PAGE_POSITIONS + cell % DSV4_PAGE_POSITIONS;
+        reinterpret_cast<uint32_t *>((kKind == kValue ? p.cache.v_codes : p.cache.k_codes) + row * (D / 2))[l] = c;
+        if ((l & 3) == 0) (kKind == kValue ? p.cache.v_scales : p.cache.k_scales)[row * (D / kKv4Block) + l / 4] = sb;
+        uint16_t *stored = kKind == kValue ? p.v_stored : p.k_stored;
+        if (stored) {
+          const float sc = __uint_as_float(sb == 255 ? 0x7FC00000u : static_cast<uint32_t>(sb) << 23);
+          uint32_t h[4];
+          e2m1x8_to_half2(c, h);
+          float y[E];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+            y[2 * i] = f.x * sc, y[2 * i + 1] = f.y * sc;
+          }
+          store_vals<E>(stored, DSV4_BF16, t0 * p.Hk * D + w.out + l * E, y);
         }
       }
     }
-    if constexpr (D <= 128) {
-      if (cached) {  // (every lane of the warp takes the shuffles)
-        float am = fabsf(x[0]);
-#pragma unroll
-        for (int i = 1; i < E; ++i) am = max_nan(am, fabsf(x[i]));
-        am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-        am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-        if (live && r.kind != 0) {
-          const int sb = block_scale(am);
-          const float up = __uint_as_float(static_cast<uint32_t>(sb == 255 ? 0 : 254 - sb) << 23);  // 2^-k
-          uint32_t w = 0;
-          if (sb != 255) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w |= e2m1_pair(x[2 * i] * up, x[2 * i + 1] * up) << (8 * i);
-          }
-          const int64_t cell = cell_sh[r.j];
-          const int64_t row = ((cell / DSV4_PAGE_POSITIONS) * p.Hk + r.h) * DSV4_PAGE_POSITIONS + cell % DSV4_PAGE_POSITIONS;
-          const bool is_v = r.kind == 2;
-          reinterpret_cast<uint32_t *>((is_v ? p.cache.v_codes : p.cache.k_codes) + row * (D / 2))[l] = w;
-          if ((l & 3) == 0) (is_v ? p.cache.v_scales : p.cache.k_scales)[row * (D / kKv4Block) + l / 4] = sb;
-          uint16_t *stored = is_v ? p.v_stored : p.k_stored;
-          if (stored) {
-            const float sc = __uint_as_float(sb == 255 ? 0x7FC00000u : static_cast<uint32_t>(sb) << 23);
-            uint32_t h[4];
-            e2m1x8_to_half2(w, h);
-            float y[E];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-              y[2 * i] = f.x * sc, y[2 * i + 1] = f.y * sc;
-            }
-            store_vals<E>(stored, DSV4_BF16, (t * p.Hk + r.h) * D + l * E, y);
-          }
-        }
-      }
+  };
+  // all rows of one kind; `raw` holds the first
+  auto pass = [&](auto kind_tag, Row raw, RowWalk w, int total, int64_t t0) {
+    constexpr int kKind = decltype(kind_tag)::value;
+    const int H = kKind == kQuery ? p.Hq : p.Hk, dj = kKind == kQuery ? djq : djk, dh = kKind == kQuery ? dhq : dhk;
+    const int64_t stride = kKind == kQuery ? p.q_stride : (kKind == kKey ? p.k_stride : p.v_stride);
+    const void *src = kKind == kQuery ? p.q : (kKind == kKey ? p.k : p.v);
+    const int64_t base = t0 * stride + l * E;
+    // as many turns for every thread of the block: the row sums are warp-wide
+    for (int at = static_cast<int>(blockIdx.y) * G; at < total; at += S) {
+      RowWalk n = w;
+      n.next(S, dj, dh, H, stride, D);
+      Row next;
+      if (n.left > 0) next.load(src, base + n.in);
+      else next.zero();
+      const bool in = w.left > 0;
+      if (!in) w.j = 0;  // (a thread without a row in the last turn)
+      finish(kind_tag, raw, w, in, t0);
+      raw = next;
+      w = n;
     }
   };
 
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * P.step; t0 < p.T; t0 += static_cast<int64_t>(P.tok_blocks) * P.step) {
     const int nt = p.T - t0 < P.step ? static_cast<int>(p.T - t0) : P.step;
-    const int total = nt * (p.Hq + (cached ? 2 : 1) * p.Hk);
     // the first rows' loads, which need no position, are under way while the positions are looked up
-    int base = static_cast<int>(blockIdx.y) * 2 * G;
-    Row ra = row_of(base + g, nt), rb = row_of(base + G + g, nt);
-    float xa[E], xb[E];
-    load_row(ra, t0, xa);
-    load_row(rb, t0, xb);
-    // the sequence of the first token: as many as end at or before it
-    __syncthreads();
-    if (tid == 0) first_sh = 0;
-    __syncthreads();
-    int before = 0;
-    for (int i = tid; i < p.B; i += kHThreads) before += p.cu_seqlens[i + 1] <= t0;
-    before = __reduce_add_sync(0xFFFFFFFFu, before);
-    if ((tid & 31) == 0 && before) atomicAdd(&first_sh, before);
-    __syncthreads();
-    if (tid < nt) {
-      const int64_t t = t0 + tid;
-      int s = first_sh;
-      while (s < p.B && p.cu_seqlens[s + 1] <= t) ++s;
-      int64_t pos = -1, cell = -1;
-      if (s < p.B && p.cu_seqlens[s] <= t) {
-        const int64_t start = p.start_pos[s];
-        if (start < 0) {
-          report(p.d_status, DSV4_DEV_BAD_LENGTH);
-        } else {
-          pos = start + (t - p.cu_seqlens[s]);
-          if (cached) {
-            const int64_t blk = pos / DSV4_PAGE_POSITIONS;
-            if (blk >= p.cache.max_blocks) {
-              report(p.d_status, DSV4_DEV_BAD_LENGTH);
-            } else {
-              const int page = p.cache.block_table[static_cast<int64_t>(s) * p.cache.max_blocks + blk];
-              if (page < 0 || page >= p.cache.num_pages) report(p.d_status, DSV4_DEV_BAD_PAGE);
-              else cell = static_cast<int64_t>(page) * DSV4_PAGE_POSITIONS + pos % DSV4_PAGE_POSITIONS;
+    RowWalk wq{}, wk{}, wv{};
+    Row rq, rk, rv;
+    rq.zero(), rk.zero(), rv.zero();
+    if (p.Hq) wq.begin(first, S, p.Hq, nt * p.Hq, p.q_stride, D);
+    if (p.Hk) wk.begin(first, S, p.Hk, nt * p.Hk, p.k_stride, D);
+    if (wq.left > 0) rq.load(p.q, t0 * p.q_stride + l * E + wq.in);
+    if (wk.left > 0) rk.load(p.k, t0 * p.k_stride + l * E + wk.in);
+    if (cached) {
+      wv.begin(first, S, p.Hk, nt * p.Hk, p.v_stride, D);
+      if (wv.left > 0) rv.load(p.v, t0 * p.v_stride + l * E + wv.in);
+    }
+    __syncthreads();  // (the step before has read its positions and angles)
+    if (tid < 32) {
+      // The sequence of the step's first token: as many as end at or before it, found 32 probes at a time.
+      int lo = 0, hi = p.B;
+      while (hi > lo) {
+        const int width = (hi - lo + 31) / 32, at = lo + (tid + 1) * width - 1;
+        const int c = __popc(__ballot_sync(0xFFFFFFFFu, at < hi && p.cu_seqlens[at + 1] <= t0));
+        hi = min(hi, lo + (c + 1) * width - 1);
+        lo += c * width;
+      }
+      if (tid < nt) {
+        const int64_t t = t0 + tid;
+        int s = lo;
+        while (s < p.B && p.cu_seqlens[s + 1] <= t) ++s;
+        int64_t pos = -1, cell = -1;
+        if (s < p.B && p.cu_seqlens[s] <= t) {
+          const int64_t start = p.start_pos[s];
+          if (start < 0) {
+            report(p.d_status, DSV4_DEV_BAD_LENGTH);
+          } else {
+            pos = start + (t - p.cu_seqlens[s]);
+            if (cached) {
+              const int64_t blk = pos / DSV4_PAGE_POSITIONS;
+              if (blk >= p.cache.max_blocks) {
+                report(p.d_status, DSV4_DEV_BAD_LENGTH);
+              } else {
+                const int page = p.cache.block_table[static_cast<int64_t>(s) * p.cache.max_blocks + blk];
+                if (page < 0 || page >= p.cache.num_pages) report(p.d_status, DSV4_DEV_BAD_PAGE);
+                else cell = static_cast<int64_t>(page) * DSV4_PAGE_POSITIONS + pos % DSV4_PAGE_POSITIONS;
+              }
             }
           }
         }
+        pos_sh[tid] = pos;
+        cell_sh[tid] = cell;
       }
-      pos_sh[tid] = pos;
-      cell_sh[tid] = cell;
     }
     __syncthreads();
     for (int i = tid; i < nt * pairs; i += kHThreads) {
       const int j = i / pairs, pr = i % pairs;
-      double c = 1.0, s = 0.0;
       if (pos_sh[j] >= 0) {
         double th = 1.0, b = p.rope_theta1;  // theta1^pr by binary powering
         for (int e = pr; e; e >>= 1) {
           if (e & 1) th *= b;
           b *= b;
         }
-        sincos(static_cast<double>(pos_sh[j]) * th, &s, &c);
+        turn[j][pr] = cos_sin(static_cast<double>(pos_sh[j]) * th);
       }
-      turn[j][pr] = make_float2(static_cast<float>(c), static_cast<float>(s));
     }
     __syncthreads();
-
-    // two rows per thread at a time; group y of the grid takes every row_split-th set of 2 G rows
-    for (;;) {
-      finish_row(ra, t0, xa);
-      finish_row(rb, t0, xb);
-      base += P.row_split * 2 * G;
-      if (base >= total) break;
-      ra = row_of(base + g, nt), rb = row_of(base + G + g, nt);
-      load_row(ra, t0, xa);
-      load_row(rb, t0, xb);
-    }
+    pass(std::integral_constant<int, kQuery>{}, rq, wq, nt * p.Hq, t0);
+    pass(std::integral_constant<int, kKey>{}, rk, wk, nt * p.Hk, t0);
+    if (cached) pass(std::integral_constant<int, kValue>{}, rv, wv, nt * p.Hk, t0);
   }
 }
 
 template <bool F32>
 cudaError_t launch_typed(HeadsParams &P, cudaStream_t st) {
   const int D = P.a.D;
-  const int64_t pass = 2 * (kHThreads / (D <= 256 ? D / 8 : 32));  // rows of a block at a time
-  const int rows = P.a.Hq + (P.a.cache.k_codes ? 2 : 1) * P.a.Hk;
-  // Few tokens: a token a step, its rows spread over blocks until the card is filled; many tokens: up to eight
-  // a step, all their rows on one block (the lookups and angles once), and blocks walk over the steps.
-  const int want = sm_count() * 8;
-  const int step = P.a.T / want;
-  P.step = step < 1 ? 1 : (step > kHTokens ? kHTokens : step);
+  const int64_t G = kHThreads / (D <= 256 ? D / 8 : 32);  // rows of a block at a time
+  // As many tokens a step, up to eight, as let all steps run at once (four blocks an SM); with fewer tokens than
+  // that, a step's rows spread over blocks; with more, blocks walk over the steps.
+  const int want = sm_count() * 4;
+  const int step = (P.a.T + want - 1) / want;
+  P.step = step > kHTokens ? kHTokens : step;
   const int steps = (P.a.T + P.step - 1) / P.step;
-  const int64_t sets = (static_cast<int64_t>(P.step) * rows + pass - 1) / pass;
+  const int64_t sets = (static_cast<int64_t>(P.step) * (P.a.Hq > P.a.Hk ? P.a.Hq : P.a.Hk) + G - 1) / G;
   P.tok_blocks = steps < want ? steps : want;
   const int64_t split = want / P.tok_blocks;
   P.row_split = static_cast<int>(split < 1 ? 1 : (split > sets ? sets : split));
-  P.div_q = P.a.Hq > 1 ? static_cast<uint32_t>(((1ull << 32) + P.a.Hq - 1) / P.a.Hq) : 0;
-  P.div_k = P.a.Hk > 1 ? static_cast<uint32_t>(((1ull << 32) + P.a.Hk - 1) / P.a.Hk) : 0;
   const dim3 grid(P.tok_blocks, P.row_split);
   switch (D) {
     case 64: return launch_pdl(kv4_heads_kernel<64, F32>, grid, dim3(kHThreads), 0, st, 1, P);

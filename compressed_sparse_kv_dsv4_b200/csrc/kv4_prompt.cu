@@ -439,7 +439,7 @@ __device__ void softmax_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const Pro
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              w[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv * nan,
+              w[k] = pack_bf16(__uint_as_float(o[8 * i + 2 * k]) * inv * nan,
                                  __uint_as_float(o[8 * i + 2 * k + 1]) * inv * nan);
             dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
           }
