@@ -10,11 +10,12 @@
 // otherwise, so k comes from the exponent and mantissa bits without a logarithm. A block that
 // holds an infinity or a NaN is stored as scale byte 255, which reads as NaN.
 //
-// One pass, bound by memory: a token's rows are its query heads, key heads and value heads;
-// D / 8 neighbouring lanes (at most a warp) hold one row, 8 values (16 bytes of bf16) each, so
-// the row's sum of squares and a block's amax are a few shuffles. A block of 256 threads takes
-// up to eight tokens at a time, two rows per thread in flight; the angles of a token are
-// worked out once, by one thread per pair and token, and shared by all its heads.
+// One pass, bound by memory: a token's rows are its query heads, key heads and value heads.
+// D / 16 neighbouring lanes hold one row, each two pieces of 8 values half a row apart (with half of the
+// channels rotated, no lane works on the other half in vain), so the row's sum of squares and a block's amax are a few
+// shuffles. A block of 256 threads takes up to eight tokens at a time, with two to three rows per thread on
+// their way into shared memory (cp.async, each thread its own pieces, so nothing waits for anything but its
+// own data); the angles of a token are worked out once, by one thread per pair and token, and shared by all its heads.
 //
 // Rounding to 4 bits makes a whole step out of one bit of float32 next to a border, so the float32
 // part is kept in the textbook's order: squares rounded, then summed (four neighbours in turn at 128
@@ -29,8 +30,8 @@ namespace dsv4 {
 namespace {
 
 constexpr int kHThreads = 256;
-constexpr int kHTokens = 8;   // tokens of a block's step, at most
-constexpr int kHPairs = 256;  // rotated pairs at most (D <= 512)
+// tokens of a block's step, at most (512 channels: by shared memory)
+__host__ __device__ constexpr int step_tokens(int D) { return D <= 256 ? 8 : 4; }
 
 struct HeadsParams {
   Kv4HeadsLaunch a;
@@ -42,21 +43,12 @@ struct HeadsParams {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// a lane's E values of a row as they lie in memory, and as floats
-template <int E, bool F32>
+// a lane's two pieces of 8 values of a row as they lie in memory, and as floats
+template <bool F32>
 struct Raw {
-  static constexpr int kWords = F32 ? E / 4 : E / 8;  // 16 bytes each
+  static constexpr int kWords = F32 ? 4 : 2;  // 16 bytes each, half of them a piece's
   uint4 w[kWords];
-  __device__ __forceinline__ void load(const void *base, int64_t off) {
-    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(base) + off * (F32 ? 4 : 2));
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = __ldcs(p + i);
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ void values(float (&x)[E]) const {
+  __device__ __forceinline__ void values(float (&x)[16]) const {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
@@ -69,18 +61,15 @@ struct Raw {
   }
 };
 
-template <int E>
-__device__ __forceinline__ void store_vals(void *base, dsv4_dtype dt, int64_t off, const float (&x)[E]) {
+// eight values x[0..7] at element `off`
+__device__ __forceinline__ void store_piece(void *base, dsv4_dtype dt, int64_t off, const float *x) {
   if (dt == DSV4_F32) {
     float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + off);
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    p[0] = make_float4(x[0], x[1], x[2], x[3]);
+    p[1] = make_float4(x[4], x[5], x[6], x[7]);
   } else {
-    uint4 *p = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + off);
-#pragma unroll
-    for (int i = 0; i < E / 8; ++i)
-      p[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
-                        pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + off) =
+        make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
   }
 }
 
@@ -101,52 +90,43 @@ __device__ __forceinline__ int block_scale(float amax) {
   return min(max(k, kKv4ExpMin), kKv4ExpMax) + 127;
 }
 
-// Sum over a row of the squares x_i^2, each rounded, in the order the file's head gives: a lane's E values
-// and the L lanes of the row.
-template <int D, int E>
-__device__ __forceinline__ float sum_squares(const float (&x)[E]) {
-  constexpr int L = D / E;
+// Sum over a row of the squares x_i^2, each rounded, in the order the file's head gives: a lane's two pieces and
+// the L = D / 16 lanes of the row. An exchange in which each lane keeps half of its columns takes half the shuffles.
+template <int D>
+__device__ __forceinline__ float sum_squares(const float (&x)[16]) {
   constexpr uint32_t kAll = 0xFFFFFFFFu;
-  if constexpr (D == 64) {  // 32 columns of two, 32 channels apart: lanes 4 apart hold a column's two
-    const int l = threadIdx.x & 7;
-    float c[8];
+  float q[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = __fmul_rn(x[i], x[i]);
-    // each exchange keeps half of the columns: lane bit 2 the first or last four, then two, then one
+  for (int i = 0; i < 16; ++i) q[i] = __fmul_rn(x[i], x[i]);
+  if constexpr (D == 64) {  // 32 columns of two channels 32 apart: a lane's pieces; lane l has columns 8 l ..
+    const int l = threadIdx.x & 3;
     float d[4], e[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float send = (l & 4) ? c[i] : c[i + 4], keep = (l & 4) ? c[i + 4] : c[i];
-      d[i] = keep + __shfl_xor_sync(kAll, send, 4);
-    }
+    for (int i = 0; i < 8; ++i) q[i] += q[i + 8];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {  // columns 16 apart: lanes 2 apart
-      const float send = (l & 2) ? d[i] : d[i + 2], keep = (l & 2) ? d[i + 2] : d[i];
-      e[i] = keep + __shfl_xor_sync(kAll, send, 2);
-    }
-    const float send = (l & 1) ? e[0] : e[1], keep = (l & 1) ? e[1] : e[0];
-    float s = keep + __shfl_xor_sync(kAll, send, 1);  // columns 8 apart: neighbouring lanes
-    // lane l now has the column of eight whose bits are l's, high to low: 4, 2 and 1 apart
-    s += __shfl_xor_sync(kAll, s, 4);
-    s += __shfl_xor_sync(kAll, s, 2);
-    return s + __shfl_xor_sync(kAll, s, 1);
-  } else {  // columns of four neighbours: a lane's E / 4, then halves onto halves
-    float c[E / 4];
+    for (int i = 0; i < 4; ++i)  // columns 16 apart: lanes 2 apart
+      d[i] = ((l & 2) ? q[i + 4] : q[i]) + __shfl_xor_sync(kAll, (l & 2) ? q[i] : q[i + 4], 2);
 #pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      c[i] = __fadd_rn(__fmul_rn(x[4 * i], x[4 * i]), __fmul_rn(x[4 * i + 1], x[4 * i + 1]));
-      c[i] = __fadd_rn(c[i], __fmul_rn(x[4 * i + 2], x[4 * i + 2]));
-      c[i] = __fadd_rn(c[i], __fmul_rn(x[4 * i + 3], x[4 * i + 3]));
-    }
+    for (int i = 0; i < 2; ++i)  // 8 apart: neighbouring lanes
+      e[i] = ((l & 1) ? d[i + 2] : d[i]) + __shfl_xor_sync(kAll, (l & 1) ? d[i] : d[i + 2], 1);
+    // the lane has two of the eight sums that are left, the others' numbers are in its lane bits: 4 apart, 2, 1
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1)
+    for (int o = 2; o > 0; o >>= 1)
 #pragma unroll
-      for (int i = 0; i < E / 4; ++i) c[i] += __shfl_xor_sync(kAll, c[i], o);
+      for (int i = 0; i < 2; ++i) e[i] += __shfl_xor_sync(kAll, e[i], o);
+    return e[0] + e[1];
+  } else {  // columns of four neighbours: four a lane
+    float c[4];
 #pragma unroll
-    for (int o = E / 8; o > 0; o >>= 1)
+    for (int i = 0; i < 4; ++i) c[i] = ((q[4 * i] + q[4 * i + 1]) + q[4 * i + 2]) + q[4 * i + 3];
+    c[0] += c[2];  // half a row apart
+    c[1] += c[3];
+    constexpr int L = D / 16;
+    const bool up = threadIdx.x & (L / 2);
+    float s = (up ? c[1] : c[0]) + __shfl_xor_sync(kAll, up ? c[0] : c[1], L / 2);
 #pragma unroll
-      for (int i = 0; i < o; ++i) c[i] += c[i + o];
-    return c[0];
+    for (int o = L / 4; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+    return s + __shfl_xor_sync(kAll, s, L / 2);
   }
 }
 
@@ -187,37 +167,37 @@ enum { kQuery, kKey, kValue };
 // token it / H. Divisions only at the start: the walk adds S = dj * H + dh.
 struct RowWalk {
   int j, h, left;      // token of the step, head, rows still to come (this one included)
-  int64_t in, out;     // element offsets of the row from the step's first token in the input and the dense output
-  __device__ __forceinline__ void begin(int first, int S, int H, int total, int64_t stride, int D) {
+  int H, dj, dh;
+  __device__ __forceinline__ void begin(int first, int S, int heads, int nt) {
+    H = heads;
+    left = 0;
+    if (H == 0) return;
+    const int total = nt * H;
     left = first < total ? (total - first + S - 1) / S : 0;
     j = first / H;
     h = first - j * H;
-    in = j * stride + h * D;
-    out = static_cast<int64_t>(first) * D;
+    dj = S / H;
+    dh = S - dj * H;
   }
-  __device__ __forceinline__ void next(int S, int dj, int dh, int H, int64_t stride, int D) {
+  __device__ __forceinline__ void next() {
     --left;
     j += dj;
     h += dh;
-    in += dj * stride + dh * D;
-    out += static_cast<int64_t>(S) * D;
-    if (h >= H) {
-      h -= H;
-      ++j;
-      in += stride - H * D;
-    }
+    if (h >= H) h -= H, ++j;
   }
 };
 
 template <int D, bool F32>
-__global__ void __launch_bounds__(kHThreads, D <= 256 ? 4 : 3) kv4_heads_kernel(const __grid_constant__ HeadsParams P) {
-  constexpr int E = D <= 256 ? 8 : D / 32;  // values of a row per lane
-  constexpr int L = D / E;                  // lanes of a row
-  constexpr int G = kHThreads / L;          // rows of a block at a time
+__global__ void __launch_bounds__(kHThreads, 3) kv4_heads_kernel(const __grid_constant__ HeadsParams P) {
+  constexpr int L = D / 16;         // lanes of a row
+  constexpr int G = kHThreads / L;  // rows of a block at a time
+  constexpr int kSize = F32 ? 4 : 2;
   const Kv4HeadsLaunch &p = P.a;
-  __shared__ __align__(16) float2 turn[kHTokens][kHPairs];  // cos and sin of a token's pairs
-  __shared__ __align__(16) float gamma[2][D];               // of queries and of keys
-  __shared__ int64_t pos_sh[kHTokens], cell_sh[kHTokens];  // position (-1: no such token), page * 256 + row (-1: none)
+  // of two neighbouring pairs both cosines, then both sines, of a token; of four neighbouring channels the even
+  // ones' weights, then the odd ones', of queries and of keys: as the packed arithmetic takes them
+  __shared__ __align__(16) float turn[step_tokens(D)][D];
+  __shared__ __align__(16) float gamma[2][D];
+  __shared__ int64_t pos_sh[step_tokens(D)], cell_sh[step_tokens(D)];  // position (-1: no such token), page * 256 + row (-1: none)
   const int tid = threadIdx.x, l = tid % L, g = tid / L;
   const bool cached = p.cache.k_codes != nullptr;
   const int pairs = p.rope_dims / 2, rope_at = D - p.rope_dims;
@@ -226,130 +206,169 @@ __global__ void __launch_bounds__(kHThreads, D <= 256 ? 4 : 3) kv4_heads_kernel(
   pdl_launch_dependents();
   for (int i = tid; i < 2 * D; i += kHThreads) {
     const float *src = i < D ? p.gamma_q : p.gamma_k;
-    gamma[i / D][i % D] = src ? src[i % D] : 1.f;
+    const int d = i % D;
+    gamma[i / D][(d & ~3) + (d & 1) * 2 + (d >> 1 & 1)] = src ? src[d] : 1.f;
   }
   const int first = static_cast<int>(blockIdx.y) * G + g, S = P.row_split * G;
-  const int djq = p.Hq ? S / p.Hq : 0, dhq = S - djq * p.Hq, djk = p.Hk ? S / p.Hk : 0, dhk = S - djk * p.Hk;
+  using Row = Raw<F32>;
+  constexpr int kDepth = F32 ? 2 : 3;  // turns whose rows are on their way
+  __shared__ uint4 ring[kDepth][Row::kWords][kHThreads];
 
-  using Row = Raw<E, F32>;
   // one row: x in, results out
-  auto finish = [&](auto kind_tag, const Row &raw, const RowWalk &w, bool in, int64_t t0) {
+  auto finish = [&](auto kind_tag, const Row &raw, const RowWalk &w, bool in, int64_t t0, int64_t out) {
     constexpr int kKind = decltype(kind_tag)::value;
-    float x[E];
+    float x[16];
     raw.values(x);
     bool live = in && pos_sh[w.j] >= 0;
     if (kKind != kQuery && cached) live = live && cell_sh[w.j] >= 0;
     if constexpr (kKind != kValue) {
       if ((kKind == kQuery ? p.gamma_q : p.gamma_k) != nullptr) {
-        const float inv = rsqrtf(__fadd_rn(sum_squares<D, E>(x) * (1.f / D), p.eps));
-        const float4 *gm = reinterpret_cast<const float4 *>(&gamma[kKind][l * E]);
+        const float inv = rsqrtf(__fadd_rn(sum_squares<D>(x) * (1.f / D), p.eps));
+        const uint64_t inv2 = pack_f32x2(inv, inv);
 #pragma unroll
-        for (int i = 0; i < E / 4; ++i) {
-          const float4 m = gm[i];
-          x[4 * i] = __fmul_rn(__fmul_rn(x[4 * i], inv), m.x);
-          x[4 * i + 1] = __fmul_rn(__fmul_rn(x[4 * i + 1], inv), m.y);
-          x[4 * i + 2] = __fmul_rn(__fmul_rn(x[4 * i + 2], inv), m.z);
-          x[4 * i + 3] = __fmul_rn(__fmul_rn(x[4 * i + 3], inv), m.w);
+        for (int i = 0; i < 16; i += 4) {
+          const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(&gamma[kKind][i / 8 * (D / 2) + l * 8 + i % 8]);
+          unpack_f32x2(mul_f32x2(mul_f32x2(pack_f32x2(x[i], x[i + 2]), inv2), m.x), x[i], x[i + 2]);
+          unpack_f32x2(mul_f32x2(mul_f32x2(pack_f32x2(x[i + 1], x[i + 3]), inv2), m.y), x[i + 1], x[i + 3]);
         }
       }
-      auto rotate = [&](int i, float c, float s) {
-        const float a = x[i], b = x[i + 1];
-        x[i] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-        x[i + 1] = __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
-      };
-      const int d0 = l * E - rope_at;  // even: rope_dims, D and E are
-      if (aligned) {
-        if (d0 + E > 0) {
-          const float4 *cs = reinterpret_cast<const float4 *>(&turn[w.j][0]) + d0 / 4;
 #pragma unroll
-          for (int i = 0; i < E; i += 4) {
-            if (E > 8 && d0 + i < 0) continue;  // (16 values of a lane, 8 of them turned)
-            const float4 v = cs[i / 4];
-            rotate(i, v.x, v.y);
-            rotate(i + 2, v.z, v.w);
+      for (int c = 0; c < 2; ++c) {
+        const int d0 = c * (D / 2) + l * 8 - rope_at;  // even: rope_dims and D are
+        if (aligned) {
+          if (d0 >= 0) {
+            const ulonglong2 *cs = reinterpret_cast<const ulonglong2 *>(&turn[w.j][d0]);
+#pragma unroll
+            for (int i = 8 * c; i < 8 * c + 8; i += 4) {
+              const ulonglong2 v = cs[(i & 4) / 4];
+              const uint64_t a = pack_f32x2(x[i], x[i + 2]), b = pack_f32x2(x[i + 1], x[i + 3]);
+              unpack_f32x2(sub_f32x2(mul_f32x2(a, v.x), mul_f32x2(b, v.y)), x[i], x[i + 2]);
+              unpack_f32x2(add_f32x2(mul_f32x2(a, v.y), mul_f32x2(b, v.x)), x[i + 1], x[i + 3]);
+            }
           }
-        }
-      } else {
+        } else {
 #pragma unroll
-        for (int i = 0; i < E; i += 2)
-          if (d0 + i >= 0) rotate(i, turn[w.j][(d0 + i) >> 1].x, turn[w.j][(d0 + i) >> 1].y);
+          for (int i = 0; i < 8; i += 2)
+            if (d0 + i >= 0) {
+              const int pr = (d0 + i) >> 1;
+              const float co = turn[w.j][(pr >> 1) * 4 + (pr & 1)], si = turn[w.j][(pr >> 1) * 4 + (pr & 1) + 2];
+              const float a = x[8 * c + i], b = x[8 * c + i + 1];
+              x[8 * c + i] = __fsub_rn(__fmul_rn(a, co), __fmul_rn(b, si));
+              x[8 * c + i + 1] = __fadd_rn(__fmul_rn(a, si), __fmul_rn(b, co));
+            }
+        }
       }
       if (kKind == kQuery || !cached) {
-        const int64_t off = t0 * (kKind == kQuery ? p.Hq : p.Hk) * D + w.out + l * E;
-        if (live) store_vals<E>(kKind == kQuery ? p.q_out : p.k_out, p.out_dt, off, x);
+        if (live) {
+          store_piece(kKind == kQuery ? p.q_out : p.k_out, p.out_dt, out, x);
+          store_piece(kKind == kQuery ? p.q_out : p.k_out, p.out_dt, out + D / 2, x + 8);
+        }
         return;
       }
     }
     if constexpr (D <= 128 && kKind != kQuery) {
-      float am = fabsf(x[0]);
-#pragma unroll
-      for (int i = 1; i < E; ++i) am = max_nan(am, fabsf(x[i]));
-      am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-      am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+      int64_t row = 0;
       if (live) {
+        const int64_t cell = cell_sh[w.j];
+        row = (cell / DSV4_PAGE_POSITIONS * p.Hk + w.h) * DSV4_PAGE_POSITIONS + cell % DSV4_PAGE_POSITIONS;
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float *y = x + 8 * c;
+        float am = fabsf(y[0]);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) am = max_nan(am, fabsf(y[i]));
+        am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+        am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+        if (!live) continue;
         const int sb = block_scale(am);
         const float up = __uint_as_float(static_cast<uint32_t>(sb == 255 ? 0 : 254 - sb) << 23);  // 2^-k
-        uint32_t c = 0;
+        uint32_t code = 0;
         if (sb != 255) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) c |= e2m1_pair(x[2 * i] * up, x[2 * i + 1] * up) << (8 * i);
+          for (int i = 0; i < 4; ++i) code |= e2m1_pair(y[2 * i] * up, y[2 * i + 1] * up) << (8 * i);
         }
-        const int64_t cell = cell_sh[w.j];
-        const int64_t row = (cell / DSV4_PAGE_POSITIONS * p.Hk + w.h) * DSV4_PAGE_POSITIONS + cell % DSV4_PAGE_POSITIONS;
-        reinterpret_cast<uint32_t *>((kKind == kValue ? p.cache.v_codes : p.cache.k_codes) + row * (D / 2))[l] = c;
-        if ((l & 3) == 0) (kKind == kValue ? p.cache.v_scales : p.cache.k_scales)[row * (D / kKv4Block) + l / 4] = sb;
+        reinterpret_cast<uint32_t *>((kKind == kValue ? p.cache.v_codes : p.cache.k_codes) + row * (D / 2))[c * (D / 16) + l] = code;
+        if ((l & 3) == 0)
+          (kKind == kValue ? p.cache.v_scales : p.cache.k_scales)[row * (D / kKv4Block) + c * (D / 64) + l / 4] = sb;
         uint16_t *stored = kKind == kValue ? p.v_stored : p.k_stored;
         if (stored) {
           const float sc = __uint_as_float(sb == 255 ? 0x7FC00000u : static_cast<uint32_t>(sb) << 23);
           uint32_t h[4];
-          e2m1x8_to_half2(c, h);
-          float y[E];
+          e2m1x8_to_half2(code, h);
+          float z[8];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-            y[2 * i] = f.x * sc, y[2 * i + 1] = f.y * sc;
+            z[2 * i] = f.x * sc, z[2 * i + 1] = f.y * sc;
           }
-          store_vals<E>(stored, DSV4_BF16, t0 * p.Hk * D + w.out + l * E, y);
+          store_piece(stored, DSV4_BF16, out + c * (D / 2), z);
         }
       }
     }
   };
-  // all rows of one kind; `raw` holds the first
-  auto pass = [&](auto kind_tag, Row raw, RowWalk w, int total, int64_t t0) {
+  // turns of a kind: as many for every thread of the block (the row sums are warp-wide)
+  auto turns_of = [&](int heads, int nt) {
+    const int rest = nt * heads - static_cast<int>(blockIdx.y) * G;
+    return rest > 0 ? (rest + S - 1) / S : 0;
+  };
+  // The step's turns, all kinds in a row, are loaded kDepth ahead; `at` walks over the rows to be loaded.
+  RowWalk at;
+  int kind = 0, to_load = 0;  // turns of the kind still to be loaded
+  const char *src = nullptr;
+  int64_t stride = 0;
+  auto load_kind = [&](int k, int nt, int64_t t0) {
+    kind = k;
+    const int heads = k == kQuery ? p.Hq : p.Hk;
+    at.begin(first, S, heads, nt);
+    to_load = k == kValue && !cached ? 0 : turns_of(heads, nt);
+    stride = (k == kQuery ? p.q_stride : (k == kKey ? p.k_stride : p.v_stride)) * kSize;
+    src = static_cast<const char *>(k == kQuery ? p.q : (k == kKey ? p.k : p.v)) + t0 * stride + l * (8 * kSize);
+  };
+  auto load_turn = [&](int slot, int nt, int64_t t0) {
+    while (to_load == 0 && kind < kValue) load_kind(kind + 1, nt, t0);
+    if (to_load > 0) {
+      if (at.left > 0) {
+        const char *row = src + at.j * stride + at.h * (D * kSize);
+        constexpr int kHalf = Row::kWords / 2;  // 16-byte words of a piece
+#pragma unroll
+        for (int i = 0; i < Row::kWords; ++i)
+          cp_async16(&ring[slot][i][tid], row + i / kHalf * (D / 2 * kSize) + i % kHalf * 16);
+      }
+      at.next();
+      --to_load;
+    }
+    cp_async_commit();
+  };
+  // all rows of one kind; `turn_no`: turns of the step so far
+  auto pass = [&](auto kind_tag, int &turn_no, int nt, int64_t t0) {
     constexpr int kKind = decltype(kind_tag)::value;
-    const int H = kKind == kQuery ? p.Hq : p.Hk, dj = kKind == kQuery ? djq : djk, dh = kKind == kQuery ? dhq : dhk;
-    const int64_t stride = kKind == kQuery ? p.q_stride : (kKind == kKey ? p.k_stride : p.v_stride);
-    const void *src = kKind == kQuery ? p.q : (kKind == kKey ? p.k : p.v);
-    const int64_t base = t0 * stride + l * E;
-    // as many turns for every thread of the block: the row sums are warp-wide
-    for (int at = static_cast<int>(blockIdx.y) * G; at < total; at += S) {
-      RowWalk n = w;
-      n.next(S, dj, dh, H, stride, D);
-      Row next;
-      if (n.left > 0) next.load(src, base + n.in);
-      else next.zero();
+    const int H = kKind == kQuery ? p.Hq : p.Hk;
+    RowWalk w;
+    w.begin(first, S, H, nt);
+    int64_t out = (t0 * H + first) * D + l * 8;
+    for (int n = turns_of(H, nt); n > 0; --n) {
+      const int slot = turn_no % kDepth;
+      ++turn_no;
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");  // this thread's part of the turn is there
       const bool in = w.left > 0;
-      if (!in) w.j = 0;  // (a thread without a row in the last turn)
-      finish(kind_tag, raw, w, in, t0);
-      raw = next;
-      w = n;
+      Row raw;
+#pragma unroll
+      for (int i = 0; i < Row::kWords; ++i) raw.w[i] = in ? ring[slot][i][tid] : make_uint4(0, 0, 0, 0);
+      load_turn(slot, nt, t0);
+      if (!in) w.j = 0;  // (no row in the last turn: the thread takes part in the warp's sums)
+      finish(kind_tag, raw, w, in, t0, out);
+      w.next();
+      out += static_cast<int64_t>(S) * D;
     }
   };
 
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * P.step; t0 < p.T; t0 += static_cast<int64_t>(P.tok_blocks) * P.step) {
     const int nt = p.T - t0 < P.step ? static_cast<int>(p.T - t0) : P.step;
     // the first rows' loads, which need no position, are under way while the positions are looked up
-    RowWalk wq{}, wk{}, wv{};
-    Row rq, rk, rv;
-    rq.zero(), rk.zero(), rv.zero();
-    if (p.Hq) wq.begin(first, S, p.Hq, nt * p.Hq, p.q_stride, D);
-    if (p.Hk) wk.begin(first, S, p.Hk, nt * p.Hk, p.k_stride, D);
-    if (wq.left > 0) rq.load(p.q, t0 * p.q_stride + l * E + wq.in);
-    if (wk.left > 0) rk.load(p.k, t0 * p.k_stride + l * E + wk.in);
-    if (cached) {
-      wv.begin(first, S, p.Hk, nt * p.Hk, p.v_stride, D);
-      if (wv.left > 0) rv.load(p.v, t0 * p.v_stride + l * E + wv.in);
-    }
+    load_kind(kQuery, nt, t0);
+#pragma unroll 1
+    for (int i = 0; i < kDepth; ++i) load_turn(i, nt, t0);
     __syncthreads();  // (the step before has read its positions and angles)
     if (tid < 32) {
       // The sequence of the step's first token: as many as end at or before it, found 32 probes at a time.
@@ -396,25 +415,29 @@ __global__ void __launch_bounds__(kHThreads, D <= 256 ? 4 : 3) kv4_heads_kernel(
           if (e & 1) th *= b;
           b *= b;
         }
-        turn[j][pr] = cos_sin(static_cast<double>(pos_sh[j]) * th);
+        const float2 cs = cos_sin(static_cast<double>(pos_sh[j]) * th);
+        turn[j][(pr >> 1) * 4 + (pr & 1)] = cs.x;
+        turn[j][(pr >> 1) * 4 + (pr & 1) + 2] = cs.y;
       }
     }
     __syncthreads();
-    pass(std::integral_constant<int, kQuery>{}, rq, wq, nt * p.Hq, t0);
-    pass(std::integral_constant<int, kKey>{}, rk, wk, nt * p.Hk, t0);
-    if (cached) pass(std::integral_constant<int, kValue>{}, rv, wv, nt * p.Hk, t0);
+    int turn_no = 0;
+    pass(std::integral_constant<int, kQuery>{}, turn_no, nt, t0);
+    pass(std::integral_constant<int, kKey>{}, turn_no, nt, t0);
+    if (cached) pass(std::integral_constant<int, kValue>{}, turn_no, nt, t0);
   }
+  cp_async_wait_all();
 }
 
 template <bool F32>
 cudaError_t launch_typed(HeadsParams &P, cudaStream_t st) {
   const int D = P.a.D;
-  const int64_t G = kHThreads / (D <= 256 ? D / 8 : 32);  // rows of a block at a time
-  // As many tokens a step, up to eight, as let all steps run at once (four blocks an SM); with fewer tokens than
+  const int64_t G = kHThreads / (D / 16);  // rows of a block at a time
+  // As many tokens a step, up to eight, as let all steps run at once (three blocks an SM); with fewer tokens than
   // that, a step's rows spread over blocks; with more, blocks walk over the steps.
-  const int want = sm_count() * 4;
+  const int want = sm_count() * 3;
   const int step = (P.a.T + want - 1) / want;
-  P.step = step > kHTokens ? kHTokens : step;
+  P.step = step > step_tokens(D) ? step_tokens(D) : step;
   const int steps = (P.a.T + P.step - 1) / P.step;
   const int64_t sets = (static_cast<int64_t>(P.step) * (P.a.Hq > P.a.Hk ? P.a.Hq : P.a.Hk) + G - 1) / G;
   P.tok_blocks = steps < want ? steps : want;
