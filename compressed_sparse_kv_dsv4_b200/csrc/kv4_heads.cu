@@ -38,7 +38,14 @@ struct HeadsParams {
   int row_split;   // blocks along y, each on every row_split-th group of rows
   int tok_blocks;  // blocks along x
   int step;        // tokens of a block's step
+  // of query rows and of key rows: heads, ceil(2^32 / heads), and S = row_split * G = dj * heads + dh
+  int heads[2], dj[2], dh[2];
+  uint32_t per_head[2], per_split;
 };
+
+// a / b by its reciprocal m = ceil(2^32 / b): exact while a * b < 2^32 (rows of a step, below 2^17, over heads up to
+// 2^14; sets of rows, below 2^18, over at most some hundred blocks)
+__device__ __forceinline__ int over(int a, int b, uint32_t m) { return b == 1 ? a : static_cast<int>(__umulhi(a, m)); }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -168,16 +175,13 @@ enum { kQuery, kKey, kValue };
 struct RowWalk {
   int j, h, left;      // token of the step, head, rows still to come (this one included)
   int H, dj, dh;
-  __device__ __forceinline__ void begin(int first, int S, int heads, int nt) {
-    H = heads;
-    left = 0;
-    if (H == 0) return;
-    const int total = nt * H;
-    left = first < total ? (total - first + S - 1) / S : 0;
-    j = first / H;
+  __device__ __forceinline__ void begin(const HeadsParams &P, int which, int first, int total, int turns, int S) {
+    H = P.heads[which];
+    dj = P.dj[which];
+    dh = P.dh[which];
+    j = over(first, H, P.per_head[which]);
     h = first - j * H;
-    dj = S / H;
-    dh = S - dj * H;
+    left = turns - (first + (turns - 1) * S >= total);  // (the last turn may have no row for this thread)
   }
   __device__ __forceinline__ void next() {
     --left;
@@ -309,8 +313,8 @@ __global__ void __launch_bounds__(kHThreads, 3) kv4_heads_kernel(const __grid_co
   };
   // turns of a kind: as many for every thread of the block (the row sums are warp-wide)
   auto turns_of = [&](int heads, int nt) {
-    const int rest = nt * heads - static_cast<int>(blockIdx.y) * G;
-    return rest > 0 ? (rest + S - 1) / S : 0;
+    const int sets = (nt * heads + G - 1) / G - static_cast<int>(blockIdx.y);
+    return sets > 0 ? over(sets + P.row_split - 1, P.row_split, P.per_split) : 0;
   };
   // The step's turns, all kinds in a row, are loaded kDepth ahead; `at` walks over the rows to be loaded.
   RowWalk at;
@@ -320,8 +324,8 @@ __global__ void __launch_bounds__(kHThreads, 3) kv4_heads_kernel(const __grid_co
   auto load_kind = [&](int k, int nt, int64_t t0) {
     kind = k;
     const int heads = k == kQuery ? p.Hq : p.Hk;
-    at.begin(first, S, heads, nt);
     to_load = k == kValue && !cached ? 0 : turns_of(heads, nt);
+    at.begin(P, k == kQuery ? 0 : 1, first, nt * heads, to_load, S);
     stride = (k == kQuery ? p.q_stride : (k == kKey ? p.k_stride : p.v_stride)) * kSize;
     src = static_cast<const char *>(k == kQuery ? p.q : (k == kKey ? p.k : p.v)) + t0 * stride + l * (8 * kSize);
   };
@@ -344,10 +348,11 @@ __global__ void __launch_bounds__(kHThreads, 3) kv4_heads_kernel(const __grid_co
   auto pass = [&](auto kind_tag, int &turn_no, int nt, int64_t t0) {
     constexpr int kKind = decltype(kind_tag)::value;
     const int H = kKind == kQuery ? p.Hq : p.Hk;
+    int n = turns_of(H, nt);
     RowWalk w;
-    w.begin(first, S, H, nt);
+    w.begin(P, kKind == kQuery ? 0 : 1, first, nt * H, n, S);
     int64_t out = (t0 * H + first) * D + l * 8;
-    for (int n = turns_of(H, nt); n > 0; --n) {
+    for (; n > 0; --n) {
       const int slot = turn_no % kDepth;
       ++turn_no;
       asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");  // this thread's part of the turn is there
@@ -443,6 +448,16 @@ cudaError_t launch_typed(HeadsParams &P, cudaStream_t st) {
   P.tok_blocks = steps < want ? steps : want;
   const int64_t split = want / P.tok_blocks;
   P.row_split = static_cast<int>(split < 1 ? 1 : (split > sets ? sets : split));
+  const int S = P.row_split * static_cast<int>(G);
+  for (int k = 0; k < 2; ++k) {
+    const int heads = k == 0 ? P.a.Hq : P.a.Hk;
+    P.heads[k] = heads;
+    if (heads == 0) continue;
+    P.dj[k] = S / heads;
+    P.dh[k] = S % heads;
+    P.per_head[k] = static_cast<uint32_t>(((1ull << 32) + heads - 1) / heads);
+  }
+  P.per_split = static_cast<uint32_t>(((1ull << 32) + P.row_split - 1) / P.row_split);
   const dim3 grid(P.tok_blocks, P.row_split);
   switch (D) {
     case 64: return launch_pdl(kv4_heads_kernel<64, F32>, grid, dim3(kHThreads), 0, st, 1, P);
