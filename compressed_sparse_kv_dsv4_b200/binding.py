@@ -422,7 +422,10 @@ class DeviceKv4Cache:
                 raise ValueError("codes and scales are contiguous uint8 tensors on the table's device")
         if bt.dtype is not _I32 or bt.dim() != 2 or not bt.is_contiguous():
             raise ValueError("block_table is a contiguous [B, max_blocks] int32 tensor")
-        return A.Kv4Cache(_ptr(kc), _ptr(vc), _ptr(ks), _ptr(vs), _ptr(bt), pages, bt.shape[1], heads, half * 2)
+        if dev < 0:
+            raise ValueError("expected a CUDA tensor")
+        return A.Kv4Cache(kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), bt.data_ptr(), pages, bt.shape[1],
+                          heads, half * 2)
 
 
 # The calls below may be a decode step's, a few microseconds of device time each, so they are written for little

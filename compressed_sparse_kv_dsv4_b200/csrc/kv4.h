@@ -1,9 +1,34 @@
 // Host-side interface of the 4-bit key/value cache kernels (kv4_*.cu), beside internal.h.
 #pragma once
 
+#include <atomic>
+
 #include "internal.h"
 
 namespace dsv4 {
+
+// launch_pdl of a kernel that takes more than 48 KiB of dynamic shared memory. The attribute that allows it is
+// set once per kernel and device (setting it costs about as much as a launch), and again where a launch
+// fails after that (a device reset drops it).
+template <auto Kernel, typename... Args>
+cudaError_t launch_large(dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args... args) {
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  for (bool again = false;; again = true) {
+    const bool set = allowed.load(std::memory_order_relaxed) & bit;
+    if (!set || again) {
+      e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      if (e != cudaSuccess) return e;
+      allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
+    e = launch_pdl(Kernel, grid, block, smem, st, 1, args...);
+    if (e == cudaSuccess || !set || again) return e;
+    cudaGetLastError();
+  }
+}
 
 constexpr int kKv4Block = 32;               // channels that share one power-of-two scale
 constexpr int kKv4ExpMin = -23;             // scale exponents: every code times its scale is then

@@ -701,9 +701,7 @@ int resident(const Kv4AttnLaunch &p) { return p.D * (tile_rows(p) / 8) <= 128 ? 
 template <int D, int NT>
 cudaError_t launch_step(AttnParams &P, cudaStream_t st) {
   const size_t smem = sizeof(AttnSmem<D, NT>) + 128;
-  cudaError_t e = cudaFuncSetAttribute(kv4_step_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(kv4_step_kernel<D, NT>, dim3(P.ctas), dim3(kThreadsA), smem, st, 1, P);
+  const cudaError_t e = launch_large<kv4_step_kernel<D, NT>>(dim3(P.ctas), dim3(kThreadsA), smem, st, P);
   if (e != cudaSuccess || P.ctas == 1) return e;
   return launch_pdl(kv4_combine_kernel<D>, dim3(P.ctas - 1), dim3(kCombineThreads), 0, st, 1, P, 8 * NT);
 }

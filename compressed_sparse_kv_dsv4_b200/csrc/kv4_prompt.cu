@@ -535,10 +535,8 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
 template <int D>
 cudaError_t launch_typed(const PromptParams &P, cudaStream_t st) {
   const size_t smem = sizeof(PromptSmem<D>) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(kv4_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kv4_prompt_kernel<D>, dim3(static_cast<unsigned>(P.row_blocks) * P.a.B * P.a.Hk), dim3(kPThreads),
-                    smem, st, 1, P);
+  return launch_large<kv4_prompt_kernel<D>>(dim3(static_cast<unsigned>(P.row_blocks) * P.a.B * P.a.Hk), dim3(kPThreads), smem,
+                                            st, P);
 }
 
 }  // namespace
