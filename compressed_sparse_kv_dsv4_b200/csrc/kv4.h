@@ -76,6 +76,11 @@ struct Kv4AttnLaunch {
 size_t kv4_attention_workspace_bytes(const Kv4AttnLaunch &p);
 cudaError_t launch_kv4_attention(const Kv4AttnLaunch &p, void *ws, cudaStream_t st);
 // the form for many rows per sequence (launch_kv4_attention chooses)
-cudaError_t launch_kv4_prompt(const Kv4AttnLaunch &p, cudaStream_t st);
+struct Kv4PromptShape {
+  int row_blocks, splits;
+};
+Kv4PromptShape kv4_prompt_shape(const Kv4AttnLaunch &p);
+size_t kv4_prompt_workspace_bytes(const Kv4AttnLaunch &p);
+cudaError_t launch_kv4_prompt(const Kv4AttnLaunch &p, void *ws, cudaStream_t st);
 
 }  // namespace dsv4

@@ -689,8 +689,23 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const __gr
   }
 }
 
-// Whether the tensor-core form for 256-row blocks takes the call.
-bool prompt_rows(const Kv4AttnLaunch &p) { return static_cast<int64_t>(p.max_new) * (p.Hq / p.Hk) > 64; }
+// Whether the tensor-core form for 256-row blocks takes the call. What it costs goes by blocks of 256 rows in waves
+// over the SMs, however few of their rows there are (1.66 us per 128 keys at 128 channels, 1.54 us at 64); the
+// step form's cost by tiles of 16 rows over the whole card (2.9 ns per 64 keys, 1.9 ns): they meet where
+// there are 283 (409) row tiles to a wave. Measured beside that, at 8 key heads, of 4 query heads each, step form and
+// the other: 8 sequences of 32768 positions, 16 new tokens (256 row tiles) 384 us and 433 us, 32 (512) 747 us
+// and 437 us. Short contexts are latency: 24 us against 15 us for 16 rows and more at 512 positions.
+bool prompt_rows(const Kv4AttnLaunch &p) {
+  const int64_t group = p.Hq / p.Hk, rows = (p.max_new < p.T ? p.max_new : p.T) * group;
+  if (rows <= 8) return false;
+  auto row_blocks = [&](int64_t size) {  // of `size` rows: at most what the longest sequence has of each, and what all tokens make
+    const int64_t by_max = p.B * ((rows + size - 1) / size), by_all = p.T * group / size + p.B;
+    return p.Hk * (by_max < by_all ? by_max : by_all);
+  };
+  const int64_t sms = sm_count(), waves = (row_blocks(256) + sms - 1) / sms;
+  if (p.cache.max_blocks <= 4 && waves <= 2) return true;
+  return row_blocks(16) * kv4_prompt_shape(p).splits > (p.D == 128 ? 283 : 409) * waves;
+}
 
 // Rows of a tile: 8 where they hold a sequence's rows, else 16. Tiles of 32 rows at 64 channels, which read and convert
 // a key once for 20 rows (5 draft tokens of 4 heads) instead of twice, were slower: 43.5 us against 34.5 us
@@ -709,13 +724,14 @@ cudaError_t launch_step(AttnParams &P, cudaStream_t st) {
 }  // namespace
 
 size_t kv4_attention_workspace_bytes(const Kv4AttnLaunch &p) {
+  if (prompt_rows(p)) return align_up(kv4_prompt_workspace_bytes(p) + 1, 256);
   const int R = tile_rows(p);
   const size_t rows = static_cast<size_t>(sm_count()) * resident(p) * 2 * R;
   return align_up(rows * p.D * sizeof(float), 256) + align_up(rows * sizeof(float2), 256);
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnLaunch &q, void *ws, cudaStream_t st) {
-  if (prompt_rows(q)) return launch_kv4_prompt(q, st);
+  if (prompt_rows(q)) return launch_kv4_prompt(q, ws, st);
   AttnParams P{};
   P.a = q;
   const int R = tile_rows(q);

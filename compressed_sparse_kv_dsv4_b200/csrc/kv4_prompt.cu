@@ -32,6 +32,9 @@ constexpr float kPOffP = 7.f;          // weights are held times 2^7
 struct PromptParams {
   Kv4AttnLaunch a;
   int row_blocks;  // blocks of 256 rows along the grid
+  int splits;      // CTAs that share a unit's keys
+  float4 *part_o;  // splits > 1: [unit][split][row tile][D / 4][128 rows], unnormalised sums
+  float2 *part_ml; // [unit][split][row tile][128 rows]: reference (log2) and sum
 };
 
 template <int D>
@@ -94,11 +97,15 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// tiles of keys that each of `splits` CTAs takes of a unit's T
+__device__ __forceinline__ int share_of(int T, int splits) { return (T + splits - 1) / splits; }
+
 // the unit of a CTA: rows 256 rb .. of one key/value head of one sequence
 struct PromptUnit {
   Seq q;
   int G, kvh;
   int64_t row0, rows;  // first row, rows of the sequence
+  int j0;              // the CTA's first tile of keys
   __device__ __forceinline__ int limit(int64_t row) const {  // positions that the row sees (0: no such row)
     if (row >= rows) return 0;
     return min(q.n, q.start + static_cast<int>(row / G) + 1);
@@ -159,7 +166,7 @@ __device__ void convert_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const Pro
       }
     }
   };
-  if (T > 0) load(0);
+  if (T > 0) load(u.j0);
   for (int j = 0; j < T; ++j, ++count) {
     uint4 k0[W], v0[W];
 #pragma unroll
@@ -167,7 +174,7 @@ __device__ void convert_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const Pro
     const uint32_t ks0 = ks;
     uint32_t vs0 = vs;
     const bool bad0 = bad;
-    if (j + 1 < T) load(j + 1);
+    if (j + 1 < T) load(u.j0 + j + 1);
     const int st = count & 1;
     if (dead) continue;
     // (K's stage is free: its last product came before event j - 2, which V of tile j - 1 waited for)
@@ -176,7 +183,7 @@ __device__ void convert_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const Pro
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&S.k_full[st]);
-    const int key = j * kKeys + r;
+    const int key = (u.j0 + j) * kKeys + r;
     if (key >= u.q.n) {
       vs0 = 0;  // not a position of the sequence: 2^-127, zero in fp16
     } else {
@@ -275,7 +282,7 @@ __device__ __forceinline__ void mma_role(PromptSmem<D> &S, uint32_t tmem, int T0
 
 template <int D>
 __device__ void softmax_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const PromptUnit &u, uint32_t tmem, int t, int T,
-                             int kv, int &done, int &units, bool &dead) {
+                             int kv, int &done, int &units, bool &dead, float4 *part_o, float2 *part_ml) {
   const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
   const uint32_t lanes = static_cast<uint32_t>(threadIdx.x & 96) << 16;
   const uint32_t s_at = tmem + 128u * t + lanes, o_at = tmem + 256u + static_cast<uint32_t>(D * t) + lanes;
@@ -325,7 +332,7 @@ __device__ void softmax_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const Pro
       break;
     }
     tc_fence_after();
-    const int key0 = j * kKeys;
+    const int key0 = (u.j0 + j) * kKeys;
     const bool edge = key0 + kKeys > least;
     const bool bad = S.bad[(kv + j) & 3];
     const int vis = bad ? 0 : lim - key0;  // columns that the row sees
@@ -407,7 +414,13 @@ __device__ void softmax_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const Pro
         tmem_ld32(o_at + c, o);
         tmem_ld_wait();
         const float nan = S.nan_at[c / kKv4Block] < lim ? __uint_as_float(0x7FC00000u) : 1.f;
-        if (lim > 0) {
+        if (part_o) {  // (a row's neighbours lie beside it, so that a warp's stores are whole lines)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            part_o[(c / 4 + i) * kRows + r] =
+                make_float4(__uint_as_float(o[4 * i]) * nan, __uint_as_float(o[4 * i + 1]) * nan,
+                            __uint_as_float(o[4 * i + 2]) * nan, __uint_as_float(o[4 * i + 3]) * nan);
+        } else if (lim > 0) {
           uint4 *dst = reinterpret_cast<uint4 *>(p.out + index * D + c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -421,7 +434,8 @@ __device__ void softmax_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const Pro
         }
       }
       tc_fence_before();
-      if (lim > 0 && p.lse) p.lse[index] = l == 0.f ? -INFINITY : (R - kPOffP + log2f(l)) * 0.6931471805599453f;
+      if (part_o) part_ml[r] = make_float2(R, l);
+      else if (lim > 0 && p.lse) p.lse[index] = l == 0.f ? -INFINITY : (R - kPOffP + log2f(l)) * 0.6931471805599453f;
     } else {
       dead = true;
     }
@@ -438,9 +452,9 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
   const int tid = threadIdx.x, warp = uniform(tid >> 5);
   constexpr uint32_t kCols = 512;
   // Blocks of later rows (more keys) come first; the sequences and heads of one block of rows are neighbours.
-  const int units = p.B * p.Hk;
-  const int first_rb = P.row_blocks - 1 - static_cast<int>(blockIdx.x) / units;
-  const int s = static_cast<int>(blockIdx.x) % units / p.Hk, kvh = static_cast<int>(blockIdx.x) % units % p.Hk;
+  const int units = p.B * p.Hk, split = static_cast<int>(blockIdx.x) % P.splits, cta = static_cast<int>(blockIdx.x) / P.splits;
+  const int first_rb = P.row_blocks - 1 - cta / units;
+  const int s = cta % units / p.Hk, kvh = cta % units % p.Hk;
   if (tid == 0) {
     mbar_init(&S.q_full, 8);
     for (int i = 0; i < 2; ++i) {
@@ -462,7 +476,9 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
   u.kvh = kvh;
   const bool any = seq_info(p, s, &u.q, tid == 0);
   u.rows = any ? static_cast<int64_t>(u.q.len) * u.G : 0;
-  if (static_cast<int64_t>(first_rb) * 2 * kRows >= u.rows) {
+  u.row0 = static_cast<int64_t>(first_rb) * 2 * kRows;
+  const int tiles = u.row0 < u.rows ? max(u.tiles(0), u.tiles(1)) : 0;
+  if (split * share_of(tiles, P.splits) >= tiles) {  // (no such rows, or nothing left for this split)
     pdl_launch_dependents();
     return;
   }
@@ -481,15 +497,24 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
   // Every role walks over the CTA's units (more than one only where a sequence brings more new
   // tokens than the call's max_new says) and meets the others before and after each.
   int kv = 0;
-  bool dead = false;
+  bool dead = false, part = false;
   // (counts that steer loops pass through a warp reduction, whose result the compiler knows to be the
   // same in all lanes: the issuing warp's operands then stay in uniform registers)
   const int64_t blocks = (u.rows + 2 * kRows - 1) / (2 * kRows) - first_rb;
-  const int turns = uniform(static_cast<int>((blocks + P.row_blocks - 1) / P.row_blocks));
+  // (the rows that max_new does not speak of have no place for parts: the first split takes them whole)
+  const int turns = split > 0 ? 1 : uniform(static_cast<int>((blocks + P.row_blocks - 1) / P.row_blocks));
   auto units_loop = [&](auto &&role) {
     for (int turn = 0; turn < turns; ++turn) {
       u.row0 = (first_rb + static_cast<int64_t>(turn) * P.row_blocks) * 2 * kRows;
-      const int T0 = uniform(u.tiles(0)), T1 = uniform(u.tiles(1));
+      int T0 = uniform(u.tiles(0)), T1 = uniform(u.tiles(1));
+      u.j0 = 0;
+      part = P.splits > 1 && turn == 0;
+      if (part) {
+        const int share = share_of(max(T0, T1), P.splits);
+        u.j0 = split * share;
+        T0 = min(max(T0 - u.j0, 0), share);
+        T1 = min(max(T1 - u.j0, 0), share);
+      }
       if (tid < D / kKv4Block) S.nan_at[tid] = 0x7FFFFFFF;
       __syncthreads();
       role(T0, T1);
@@ -501,7 +526,10 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
     more_registers<184>();
     int done = 0, n_units = 0;
     units_loop([&](int T0, int T1) {
-      softmax_role<D>(p, S, u, tmem, warp / 4, warp < 4 ? T0 : T1, kv, done, n_units, dead);
+      const int t = warp / 4;
+      const int64_t slot = part ? (static_cast<int64_t>(first_rb * units + cta % units) * P.splits + split) * 2 + t : 0;
+      softmax_role<D>(p, S, u, tmem, t, t == 0 ? T0 : T1, kv, done, n_units, dead,
+                      part ? P.part_o + slot * (D / 4 * kRows) : nullptr, part ? P.part_ml + slot * kRows : nullptr);
     });
   } else if (warp < 12) {
     fewer_registers<96>();
@@ -532,25 +560,103 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
   }
 }
 
+// Joins the splits of a unit: a block takes 32 channels of the 128 rows of a row tile, a thread a row.
+template <int D>
+__global__ void __launch_bounds__(kRows) kv4_prompt_combine_kernel(const __grid_constant__ PromptParams P) {
+  const Kv4AttnLaunch &p = P.a;
+  const int units = p.B * p.Hk, t = blockIdx.x & 1, unit = static_cast<int>(blockIdx.x >> 1), r = threadIdx.x;
+  const int rb = unit / units, s = unit % units / p.Hk, c0 = blockIdx.y * 32;
+  // (this grid starts once every CTA of the first kernel is past its own wait: the lengths can be read)
+  PromptUnit u;
+  u.G = p.Hq / p.Hk;
+  u.kvh = unit % units % p.Hk;
+  const bool any = seq_info(p, s, &u.q, false);
+  u.rows = any ? static_cast<int64_t>(u.q.len) * u.G : 0;
+  u.row0 = static_cast<int64_t>(rb) * 2 * kRows;
+  const int64_t row = u.row0 + t * kRows + r;
+  int parts = 0;
+  if (u.row0 < u.rows) {
+    const int Tt = u.tiles(t), share = share_of(max(u.tiles(0), u.tiles(1)), P.splits);
+    parts = (Tt + share - 1) / share;
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (row >= u.rows) return;
+  const int64_t index = (u.q.tok0 + row / u.G) * p.Hq + u.kvh * u.G + row % u.G;
+  const int64_t slot0 = static_cast<int64_t>(unit) * P.splits * 2 + t;
+  float top = -INFINITY;
+  for (int k = 0; k < parts; ++k) top = fmaxf(top, P.part_ml[(slot0 + 2 * k) * kRows + r].x);
+  float sum = 0.f, acc[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+#pragma unroll 2
+  for (int k = 0; k < parts; ++k) {
+    const float2 ml = P.part_ml[(slot0 + 2 * k) * kRows + r];
+    const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2_approx(ml.x - top);
+    sum = fmaf(ml.y, f, sum);
+    const float4 *src = P.part_o + (slot0 + 2 * k) * (D / 4 * kRows) + c0 / 4 * kRows + r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 v = src[i * kRows];
+      acc[4 * i] = fmaf(v.x, f, acc[4 * i]), acc[4 * i + 1] = fmaf(v.y, f, acc[4 * i + 1]);
+      acc[4 * i + 2] = fmaf(v.z, f, acc[4 * i + 2]), acc[4 * i + 3] = fmaf(v.w, f, acc[4 * i + 3]);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint4 *dst = reinterpret_cast<uint4 *>(p.out + index * D + c0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    dst[i] = make_uint4(pack_bf16(acc[8 * i] * inv, acc[8 * i + 1] * inv), pack_bf16(acc[8 * i + 2] * inv, acc[8 * i + 3] * inv),
+                        pack_bf16(acc[8 * i + 4] * inv, acc[8 * i + 5] * inv), pack_bf16(acc[8 * i + 6] * inv, acc[8 * i + 7] * inv));
+  if (c0 == 0 && p.lse) p.lse[index] = sum == 0.f ? -INFINITY : (top - kPOffP + log2f(sum)) * 0.6931471805599453f;
+}
+
+size_t part_rows(const Kv4AttnLaunch &p) {  // rows of all parts
+  const Kv4PromptShape g = kv4_prompt_shape(p);
+  return g.splits == 1 ? 0 : static_cast<size_t>(g.row_blocks) * p.B * p.Hk * g.splits * 2 * kRows;
+}
+
 template <int D>
 cudaError_t launch_typed(const PromptParams &P, cudaStream_t st) {
   const size_t smem = sizeof(PromptSmem<D>) + 1024;
-  return launch_large<kv4_prompt_kernel<D>>(dim3(static_cast<unsigned>(P.row_blocks) * P.a.B * P.a.Hk), dim3(kPThreads), smem,
-                                            st, P);
+  const unsigned units = static_cast<unsigned>(P.row_blocks) * P.a.B * P.a.Hk;
+  const cudaError_t e = launch_large<kv4_prompt_kernel<D>>(dim3(units * P.splits), dim3(kPThreads), smem, st, P);
+  if (e != cudaSuccess || P.splits == 1) return e;
+  return launch_pdl(kv4_prompt_combine_kernel<D>, dim3(2 * units, D / 32), dim3(kRows), 0, st, 1, P);
 }
 
 }  // namespace
 
-cudaError_t launch_kv4_prompt(const Kv4AttnLaunch &q, cudaStream_t st) {
-  PromptParams P{};
-  P.a = q;
-  // blocks of 256 rows of the longest sequence; the grid has at most 2^30 CTAs (a CTA walks on over the rest)
-  const int64_t most = q.max_new < q.T ? q.max_new : q.T;
-  int64_t blocks = (most * (q.Hq / q.Hk) + 2 * kRows - 1) / (2 * kRows);
-  const int64_t room = (int64_t(1) << 30) / (static_cast<int64_t>(q.B) * q.Hk);
+// Blocks of 256 rows of the longest sequence, and CTAs per block. With at most half as many blocks as SMs the keys are
+// split too (one wave of CTAs, four tiles of 128 keys each at least of the longest context that the table holds).
+Kv4PromptShape kv4_prompt_shape(const Kv4AttnLaunch &p) {
+  Kv4PromptShape g;
+  const int64_t heads = static_cast<int64_t>(p.B) * p.Hk;
+  const int64_t most = p.max_new < p.T ? p.max_new : p.T;
+  int64_t blocks = (most * (p.Hq / p.Hk) + 2 * kRows - 1) / (2 * kRows);
+  const int64_t room = (int64_t(1) << 30) / heads;  // (a CTA walks on over rows beyond the grid)
   if (blocks > room) blocks = room;
   if (blocks < 1) blocks = 1;
-  P.row_blocks = static_cast<int>(blocks);
+  g.row_blocks = static_cast<int>(blocks);
+  const int64_t sms = sm_count(), tiles = static_cast<int64_t>(p.cache.max_blocks) * (DSV4_PAGE_POSITIONS / kKeys);
+  int64_t splits = sms / (blocks * heads);
+  if (splits > tiles / 4) splits = tiles / 4;
+  g.splits = splits < 2 ? 1 : static_cast<int>(splits);
+  return g;
+}
+
+size_t kv4_prompt_workspace_bytes(const Kv4AttnLaunch &p) {
+  return align_up(part_rows(p) * p.D * sizeof(float), 256) + align_up(part_rows(p) * sizeof(float2), 256);
+}
+
+cudaError_t launch_kv4_prompt(const Kv4AttnLaunch &q, void *ws, cudaStream_t st) {
+  PromptParams P{};
+  P.a = q;
+  const Kv4PromptShape g = kv4_prompt_shape(q);
+  P.row_blocks = g.row_blocks;
+  P.splits = g.splits;
+  P.part_o = static_cast<float4 *>(ws);
+  P.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(ws) + align_up(part_rows(q) * q.D * sizeof(float), 256));
   return q.D == 64 ? launch_typed<64>(P, st) : launch_typed<128>(P, st);
 }
 
