@@ -202,17 +202,28 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   return d;
 }
 
+// four 8x8 matrices of 16-bit values from shared memory; lane i gives the address of row i % 8 of matrix i / 8
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
 // Row of a 16-key group that fragment row g (0..7) stands for: neighbouring pairs differ in parity
 // (a quarter warp's 16-byte reads of two 64-byte rows touch all banks), and so do the even ones
 // (the four rows of a value read meet two to a bank, not four).
 __device__ __forceinline__ int key_of(int g) { return (g & 4) + ((0x2130 >> (4 * (g & 3))) & 3); }
 
+// CTAs of an SM, at 128, 168 or 255 registers a thread. (Four with eight rows at 128 channels against three: 263 us and
+// 272 us for four sequences of 262144; but with 16 rows the sums spill, 42 us against 34 us for draft tokens.)
+constexpr int resident_ctas(int D, int NT) { return NT == 1 ? 4 : (D == 64 ? 3 : 2); }
+
 template <int D, int NT>
 struct StepShape {
   static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / kKv4Block;
   static constexpr int kHalf = kCodes + kScales;   // keys or values of a tile
-  static constexpr int kStages = D == 128 ? 3 : 4;  // of a warp, half a tile each
-  static constexpr int kResident = D * NT <= 128 ? 3 : 2;  // CTAs of an SM: 168 or 255 registers a thread
+  static constexpr int kStages = D == 64 ? 4 : (NT == 1 ? 2 : 3);  // of a warp, half a tile each
+  static constexpr int kResident = resident_ctas(D, NT);
 };
 
 template <int D, int NT>
@@ -221,6 +232,9 @@ struct alignas(128) AttnSmem {
   struct alignas(128) Stage {
     uint8_t c[Sh::kCodes], s[Sh::kScales];
   } stage[kWarps][Sh::kStages];
+  // Q as the first product's fragments: of row r, 8 values for each step and half of it, two per lane of the four
+  // (rows 16 bytes more than a multiple of 128 apart: the eight rows of a matrix meet different banks)
+  uint16_t q[8 * NT][D + 8];
   float o[kWarps][8 * NT][D + 4];  // the warps' sums, joined at the end of a unit's part
   float2 ml[kWarps][8 * NT];
   int64_t index[8 * NT];           // [token][head] of the unit's rows
@@ -261,6 +275,7 @@ __global__ void __launch_bounds__(kThreadsA, StepShape<D, NT>::kResident)
   fence_proxy_async_global();  // the cache's rows may come from the kernel before, by plain stores
 
   const int g = lane >> 2, t4 = lane & 3;
+  const uint32_t q_at = smem_u32(&S.q[lane & 7][8 * (lane >> 3)]);
   uint32_t issued = 0, used = 0;  // this warp's tiles
   bool dead = false;
   // The warp's next half tile into its next stage: keys (half 0) or values of tile t of u's unit. Lane 0 copies the
@@ -365,7 +380,8 @@ __global__ void __launch_bounds__(kThreadsA, StepShape<D, NT>::kResident)
 #pragma unroll
         for (int i = 0; i < KS * 2; ++i) {
           const uint32_t raw = qf[nt][i >> 1][i & 1];
-          qf[nt][i >> 1][i & 1] = pack_half2(__uint_as_float(raw << 16) * up, __uint_as_float(raw & 0xFFFF0000u) * up);
+          const uint32_t h = pack_half2(__uint_as_float(raw << 16) * up, __uint_as_float(raw & 0xFFFF0000u) * up);
+          if (warp == 0) *reinterpret_cast<uint32_t *>(&S.q[8 * nt + g][8 * i + 2 * t4]) = h;
         }
         const float mine = p.softmax_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
         rs[nt][0] = __shfl_sync(0xFFFFFFFFu, mine, 8 * t4);      // lane 4 * (2 t4): column 2 t4
@@ -425,12 +441,15 @@ __global__ void __launch_bounds__(kThreadsA, StepShape<D, NT>::kResident)
             uint32_t ha[4], hb[4];
             e2m1x8_to_half2(ca[c], ha);
             e2m1x8_to_half2(cb[c], hb);
+            uint32_t qb[NT][4];  // steps 2 c and 2 c + 1, both halves
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) ldmatrix4(qb[nt], q_at + nt * static_cast<uint32_t>(8 * sizeof(S.q[0])) + 64 * c);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const uint32_t a0 = hmul2(ha[2 * k], sa), a2 = hmul2(ha[2 * k + 1], sa);
               const uint32_t a1 = hmul2(hb[2 * k], sb), a3 = hmul2(hb[2 * k + 1], sb);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16816(s[mt][nt], a0, a1, a2, a3, qf[nt][2 * c + k][0], qf[nt][2 * c + k][1]);
+              for (int nt = 0; nt < NT; ++nt) mma16816(s[mt][nt], a0, a1, a2, a3, qb[nt][2 * k], qb[nt][2 * k + 1]);
             }
           }
         }
@@ -707,11 +726,19 @@ bool prompt_rows(const Kv4AttnLaunch &p) {
   return row_blocks(16) * kv4_prompt_shape(p).splits > (p.D == 128 ? 283 : 409) * waves;
 }
 
-// Rows of a tile: 8 where they hold a sequence's rows, else 16. Tiles of 32 rows at 64 channels, which read and convert
-// a key once for 20 rows (5 draft tokens of 4 heads) instead of twice, were slower: 43.5 us against 34.5 us
-// for 13 sequences of up to 9001 tokens (255 registers a thread, two CTAs an SM).
-int tile_rows(const Kv4AttnLaunch &p) { return static_cast<int64_t>(p.max_new) * (p.Hq / p.Hk) <= 8 ? 8 : 16; }
-int resident(const Kv4AttnLaunch &p) { return p.D * (tile_rows(p) / 8) <= 128 ? 3 : 2; }
+// Rows of a tile: 16 read and convert a key once for what takes 8 twice (2.9 ns against 2 x 2.0 ns per 64 keys), but a
+// warp's turn takes twice as long, which shows where there are few: with less than eight turns of 8 rows for
+// each of the SMs' twelve warps, going by the longest context that the table holds, 8 it is (16 rows over 4096
+// positions of one sequence 22 us against 29 us, over 32768 of eight 146 us against 114 us). Tiles of 32 rows at 64
+// channels were slower yet: 43.5 us against 34.5 us for 13 sequences of 20 rows and up to 9001 tokens.
+int tile_rows(const Kv4AttnLaunch &p) {
+  const int64_t group = p.Hq / p.Hk, rows = (p.max_new < p.T ? p.max_new : p.T) * group;
+  if (rows <= 8) return 8;
+  const int64_t by_max = p.B * ((rows + 7) / 8), by_all = p.T * group / 8 + p.B;
+  const int64_t turns = p.Hk * (by_max < by_all ? by_max : by_all) * p.cache.max_blocks * (DSV4_PAGE_POSITIONS / kTile);
+  return turns < int64_t(8) * 12 * sm_count() ? 8 : 16;
+}
+int resident(const Kv4AttnLaunch &p) { return resident_ctas(p.D, tile_rows(p) / 8); }
 
 template <int D, int NT>
 cudaError_t launch_step(AttnParams &P, cudaStream_t st) {
