@@ -471,6 +471,8 @@ def _lengths(cu_seqlens, start_pos, device: int) -> int:
 def _out(name, t, like, dtype):
     """A dense tensor of like's shape: new, or the caller's after a check."""
     if t is None:
+        if like.dtype is dtype and like.is_contiguous():
+            return torch.empty_like(like)
         return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
     if t.shape != like.shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != like.get_device():
         raise ValueError(f"{name} is a contiguous {tuple(like.shape)} {dtype} tensor on the inputs' device")
@@ -629,7 +631,7 @@ def kv4_attention(q, cu_seqlens, start_pos, cache: DeviceKv4Cache, *, max_new: i
     if out is None:
         out = _out("out", None, q, _BF16)
     if with_lse and lse is None:
-        lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
+        lse = q.new_empty(q.shape[:2], dtype=_F32)
     a = kv4_attention_args(q, cu_seqlens, start_pos, cache, max_new=max_new, softmax_scale=softmax_scale, out=out,
                            lse=lse, d_status=d_status)
     if workspace is None:

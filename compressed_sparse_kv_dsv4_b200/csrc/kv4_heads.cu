@@ -143,20 +143,22 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-// Sine and cosine of `a` (finite, |a| below 2^31), to about 1e-11 absolute, rounded once to float32: the nearest
-// multiple k of pi/2 is taken off with two constants (pi/2 to 107 bits), the rest, within pi/4, goes into
-// the Taylor polynomials up to r^11 and r^12 (next terms 7e-12 and 4e-13), and k's low bits turn the quadrant. The
+// Sine and cosine of `a` (finite, |a| below 2^31), to about 1e-13 absolute beside the angle's own rounding, rounded once to
+// float32: the nearest multiple k of pi/2 is taken off with two constants (pi/2 to 107 bits), the rest, within pi/4, goes
+// into the Taylor polynomials up to r^13 and r^14 (next terms 2e-14 and 1e-15), and k's low bits turn the quadrant. The
 // library's float64 sincos took the step of one token from 4.4 to 15 us where few pairs are worked out per block.
 __device__ __forceinline__ float2 cos_sin(double a) {
   constexpr double kHi = 1.5707963267948966, kLo = 6.123233995736766e-17, kInv = 0.6366197723675814;
   const double k = rint(a * kInv);
   const double r = fma(-k, kLo, fma(-k, kHi, a)), q = r * r;
-  double s = fma(q, -1.0 / 39916800.0, 1.0 / 362880.0);
+  double s = fma(q, 1.0 / 6227020800.0, -1.0 / 39916800.0);
+  s = fma(s, q, 1.0 / 362880.0);
   s = fma(s, q, -1.0 / 5040.0);
   s = fma(s, q, 1.0 / 120.0);
   s = fma(s, q, -1.0 / 6.0);
   s = fma(s * q, r, r);
-  double c = fma(q, 1.0 / 479001600.0, -1.0 / 3628800.0);
+  double c = fma(q, -1.0 / 87178291200.0, 1.0 / 479001600.0);
+  c = fma(c, q, -1.0 / 3628800.0);
   c = fma(c, q, 1.0 / 40320.0);
   c = fma(c, q, -1.0 / 720.0);
   c = fma(c, q, 1.0 / 24.0);
