@@ -436,6 +436,8 @@ def _elsewhere(device: int, stream) -> contextlib.ExitStack | None:
     the tensors'. Otherwise a context that makes it so (outputs are then allocated there too)."""
     if stream is None and (device < 0 or device == torch.cuda.current_device()):
         return None
+    if stream is not None and stream.device.index != device:
+        raise ValueError("the stream and the tensors are on different devices")
     ctx = contextlib.ExitStack()
     if device >= 0:
         ctx.enter_context(torch.cuda.device(device))
@@ -454,6 +456,8 @@ def _rows(name: str, t, device: int, dtype, heads: int = 0, dim: int = 0):
     st, sh, sd = t.stride()
     if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{name}: the heads of a token are contiguous rows")
+    if T > 1 and st < H * D:  # (an expanded tensor's stride is 0, which the library takes as dense)
+        raise ValueError(f"{name}: the tokens' rows overlap")
     return _ptr(t), H, (st if T > 1 else H * D)
 
 

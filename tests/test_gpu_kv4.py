@@ -78,10 +78,14 @@ NORM = [  # dim, q heads, k heads, lengths, starts, rope dims, input, output, ex
     (64, 0, 1, [300], [40], 16, "bf16", "bf16", 2),
     (128, 3, 0, [7], [1], 0, "f32", "f32", 0),
     (128, 16, 2, [1] * 70, list(range(70)), 64, "bf16", "bf16", 0),
+    (128, 6, 2, [50, 3], [17, 70000], 20, "f32", "bf16", 0),   # rotated channels that end inside a lane's eight
+    (64, 11, 1, [9], [1], 62, "bf16", "f32", 0),
+    (512, 1, 1, [33], [5], 2, "f32", "f32", 0),
+    (64, 700, 300, [5], [3], 64, "bf16", "bf16", 0),
 ]
 
 
-@pytest.mark.parametrize("case", NORM, ids=lambda c: f"D{c[0]}-{c[6]}-{len(c[3])}")
+@pytest.mark.parametrize("case", NORM, ids=lambda c: f"D{c[0]}-{c[1]}and{c[2]}-{c[6]}-{len(c[3])}")
 def test_norm_rope(case):
     require_gpu()
     D, Hq, Hk, lens, starts, rope, din, dout, extra = case
@@ -167,10 +171,11 @@ APPEND = [  # dim, q heads, kv heads, lengths, starts, rope, dtype, extra heads
     (128, 6, 2, [17, 2, 520], [250, 0, 1], 128, "bf16", 10),
     (64, 7, 1, [33], [1 << 18], 0, "f32", 3),
     (64, 12, 12, [5, 6], [0, 255], 64, "bf16", 0),
+    (128, 3, 5, [40, 9], [3, 255], 44, "bf16", 2),
 ]
 
 
-@pytest.mark.parametrize("case", APPEND, ids=lambda c: f"D{c[0]}-{c[6]}-{len(c[3])}")
+@pytest.mark.parametrize("case", APPEND, ids=lambda c: f"D{c[0]}-{c[2]}-{c[6]}-{len(c[3])}")
 def test_append(case):
     require_gpu()
     D, Hq, Hk, lens, starts, rope, din, extra = case
@@ -318,7 +323,7 @@ def test_attention(case):
     q, _ = rand_rows(rng, sum(lens), Hq, D, torch.bfloat16, 2)
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
     first = None
-    for max_new in (max(lens), 1, 5000):  # a hint: any value gives right results
+    for max_new in (max(lens), 1, 17, 5000):  # a hint: any value gives right results
         out, lse = dsv4.kv4_attention(q, cu_of(lens), i32(starts), c, max_new=max_new, with_lse=True, d_status=st)
         assert st.item() == 0
         check_attention(c, q, lens, starts, out, lse, sample=24, ctx=f"max_new {max_new}")
@@ -337,11 +342,85 @@ def test_attention_of_many_sequences():
     B = 403
     lens = [0 if i % 7 == 3 else 1 for i in range(B)]
     starts = [int(i * 37 % 90) for i in range(B)]
-    c = make_cache(rng, lens, starts, 1, 64, fill=0xFF)
+    c = make_cache(rng, lens, starts, 1, 64, fill=0xC8)  # rows behind the ends hold scales that are infinite in fp16
     fill_cache(rng, c, lens, starts)
     q, _ = rand_rows(rng, sum(lens), 2, 64, torch.bfloat16)
-    out, lse = dsv4.kv4_attention(q, cu_of(lens), i32(starts), c, max_new=1, with_lse=True)
-    check_attention(c, q, lens, starts, out, lse)
+    for max_new in (1, 5):
+        out, lse = dsv4.kv4_attention(q, cu_of(lens), i32(starts), c, max_new=max_new, with_lse=True)
+        check_attention(c, q, lens, starts, out, lse)
+
+
+@pytest.mark.parametrize("Hq,Hk,lens,starts", [(4, 1, [300], [9000]), (16, 2, [33, 1], [5000, 7000]), (8, 1, [700, 300], [3000, 0])])
+def test_attention_splits_the_keys_of_few_rows(Hq, Hk, lens, starts):
+    """Few blocks of rows over a long context: the keys are shared out; a hint that is too small leaves rows to walk on over."""
+    require_gpu()
+    rng = np.random.default_rng(21)
+    c = make_cache(rng, lens, starts, Hk, 64, fill=0xFF)
+    fill_cache(rng, c, lens, starts)
+    q, _ = rand_rows(rng, sum(lens), Hq, 64, torch.bfloat16)
+    for max_new in (max(lens), max(lens) // 3, 20):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = dsv4.kv4_attention(q, cu_of(lens), i32(starts), c, max_new=max_new, with_lse=True, d_status=st)
+        assert st.item() == 0
+        check_attention(c, q, lens, starts, out, lse, sample=12, ctx=f"max_new {max_new}")
+
+
+def test_a_cache_of_more_than_32_bits():
+    """Codes beyond 2^32 bytes: the last pages of a pool of 36000 (4.7 GB of keys, as much of values)."""
+    require_gpu()
+    rng = np.random.default_rng(22)
+    pages = 36000
+    bt = i32([[pages - 1, 3], [pages - 2, pages - 3]])
+    c = dsv4.DeviceKv4Cache.zeros(pages, 8, 128, bt)
+    assert c.k_codes.numel() > 1 << 32
+    for new in (1, 100):
+        lens, starts = [new, new], [300, 200]
+        fill_cache(rng, c, lens, starts)
+        q, _ = rand_rows(rng, 2 * new, 16, 128, torch.bfloat16)
+        out, lse = dsv4.kv4_attention(q, cu_of(lens), i32(starts), c, max_new=new, with_lse=True)
+        check_attention(c, q, lens, starts, out, lse, sample=6)
+    assert not c.k_codes[4:pages - 3].any()
+
+
+def test_the_first_call_may_be_captured():
+    """A process whose first attention and append are inside a graph capture (modules load lazily)."""
+    require_gpu()
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch, compressed_sparse_kv_dsv4_b200 as dsv4
+dsv4.load()
+def i32(v): return torch.tensor(v, dtype=torch.int32, device='cuda')
+runs = []
+for new in (1, 200):
+    c = dsv4.DeviceKv4Cache.zeros(8, 1, 64, i32([[1, 2]]))
+    q = torch.randn(new, 4, 64, device='cuda').bfloat16()
+    k = torch.randn(new, 1, 64, device='cuda').bfloat16()
+    cu, start = i32([0, new]), i32([0])
+    ws = dsv4.kv4_attention_workspace(q, cu, c, max_new=new)
+    out = torch.empty_like(q)
+    runs.append((c, q, k, cu, start, ws, out, new))
+def go(r):
+    c, q, k, cu, start, ws, out, new = r
+    dsv4.kv4_append(k, k, cu, start, c, rope_dims=0)
+    dsv4.kv4_attention(q, cu, start, c, max_new=new, out=out, workspace=ws)
+for r in runs:
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        go(r)
+    g.replay()
+    torch.cuda.synchronize()
+    got = r[6].clone()
+    go(r)
+    torch.cuda.synchronize()
+    assert torch.equal(got, r[6])
+print('captured')
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("new", [3, 200])
@@ -392,6 +471,22 @@ def test_attention_nan_stays_with_the_rows_that_see_it(new, Hq):
         assert torch.equal(out.isnan(), want) and torch.equal(lse.isnan(), want[..., 0])
         assert torch.equal(out[~sees], clean[~sees])
         c.k_scales[page, 0, row, 1] = old
+
+
+@pytest.mark.parametrize("new", [4, 300])
+def test_attention_of_a_nan_query_is_that_rows_alone(new):
+    require_gpu()
+    rng = np.random.default_rng(19)
+    c = make_cache(rng, [new], [100], 1, 64)
+    fill_cache(rng, c, [new], [100])
+    q, _ = rand_rows(rng, new, 2, 64, torch.bfloat16)
+    clean, lse0 = dsv4.kv4_attention(q, cu_of([new]), i32([100]), c, max_new=new, with_lse=True)
+    q = q.clone()
+    q[2, 1, 5] = float("nan")
+    out, lse = dsv4.kv4_attention(q, cu_of([new]), i32([100]), c, max_new=new, with_lse=True)
+    assert out[2, 1].isnan().all() and lse[2, 1].isnan()
+    out[2, 1], lse[2, 1] = clean[2, 1], lse0[2, 1]
+    assert torch.equal(out, clean) and torch.equal(lse, lse0)
 
 
 @pytest.mark.parametrize("new", [1, 40, 300])
@@ -486,6 +581,25 @@ def test_a_layers_run(D, Hq, Hk):
         ends = ends + np.array(new)
 
 
+def test_no_tokens():
+    require_gpu()
+    c = make_cache(np.random.default_rng(1), [4, 4], [0, 0], 2, 64)
+    none = torch.empty((0, 4, 64), dtype=torch.bfloat16, device="cuda")
+    cu, start = i32([0, 0, 0]), i32([5, 0])
+    out, lse = dsv4.kv4_attention(none, cu, start, c, max_new=1, with_lse=True)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    q, k, v = dsv4.kv4_append(none[:, :2], none[:, :2], cu, start, c, q=none, with_stored=True)
+    assert q.shape == (0, 4, 64) and k.shape == v.shape == (0, 2, 64)
+    assert dsv4.qk_norm_rope(none, none[:, :2], cu, start)[1].shape == (0, 2, 64)
+    # tokens, but none of them any sequence's
+    some = torch.ones((300, 4, 64), dtype=torch.bfloat16, device="cuda")
+    for max_new in (1, 300):
+        out = torch.full_like(some, 3.0)
+        dsv4.kv4_attention(some, cu, start, c, max_new=max_new, out=out)
+        assert torch.all(out == 3)
+    assert torch.all(c.k_codes == 0)
+
+
 def test_streams_and_graphs():
     """Another stream than the current one; two graphs with workspaces of their own, replayed together
     with changed contents (lengths included: they are read on the device)."""
@@ -556,6 +670,8 @@ def test_the_binding_refuses():
         a.update({n: v for n, v in bad.items() if n in a})
         with pytest.raises((ValueError, dsv4.Dsv4Error)):
             dsv4.kv4_attention(a["q"], a["cu"], a["start"], c, **ok, **more)
+    with pytest.raises(ValueError):  # expanded: all tokens are one row
+        dsv4.kv4_attention(q[:1].expand(8, 4, 64), cu, start, c, max_new=4)
     with pytest.raises(dsv4.Dsv4Error):
         dsv4.kv4_attention(q, cu, start, c, max_new=0)
     with pytest.raises(dsv4.Dsv4Error):
