@@ -77,7 +77,8 @@ size_t kv4_attention_workspace_bytes(const Kv4AttnLaunch &p);
 cudaError_t launch_kv4_attention(const Kv4AttnLaunch &p, void *ws, cudaStream_t st);
 // the form for many rows per sequence (launch_kv4_attention chooses)
 struct Kv4PromptShape {
-  int row_blocks, splits;
+  int row_blocks;     // blocks of 256 rows of each sequence and key/value head
+  int whole, splits;  // units that one CTA takes; CTAs of each of the others
 };
 Kv4PromptShape kv4_prompt_shape(const Kv4AttnLaunch &p);
 size_t kv4_prompt_workspace_bytes(const Kv4AttnLaunch &p);

@@ -725,7 +725,8 @@ bool prompt_rows(const Kv4AttnLaunch &p) {
   };
   const int64_t sms = sm_count(), waves = (row_blocks(256) + sms - 1) / sms;
   if (p.cache.max_blocks <= 4 && waves <= 2) return true;
-  return row_blocks(16) * kv4_prompt_shape(p).splits > (p.D == 128 ? 283 : 409) * waves;
+  const Kv4PromptShape g = kv4_prompt_shape(p);
+  return row_blocks(16) * (g.whole == 0 ? g.splits : 1) > (p.D == 128 ? 283 : 409) * waves;
 }
 
 // Rows of a tile: 16 read and convert a key once for what takes 8 twice (2.9 ns against 2 x 2.0 ns per 64 keys), but a

@@ -17,7 +17,7 @@
 // tile's maximum exceeds it by more than 2^8; weights are held times 2^7, at most 2^15 in fp16.
 // With few blocks of rows the keys of a block are split over CTAs, which a second kernel joins.
 // Measured: eight prompts of 4096 tokens, 32 heads over 8 of 128 channels, 1150 us (956 TFLOP/s); 2048 tokens behind
-// 14336 457 us (1129 TFLOP/s); a tile pair of 256 x 128 takes 1.85 us, 1342 TFLOP/s.
+// 14336 442 us (1165 TFLOP/s; 457 us without the last wave shared out); a tile pair of 256 x 128 takes 1.85 us, 1342 TFLOP/s.
 // A thread keeps its S row in 128 registers between the maximum and the weights (the warpgroups'
 // registers are split 184, 184, 96, 48), and hands its weights over in halves of 64 keys.
 #include "kv4_device.cuh"
@@ -35,9 +35,10 @@ constexpr float kPOffP = 7.f;          // weights are held times 2^7
 struct PromptParams {
   Kv4AttnLaunch a;
   int row_blocks;  // blocks of 256 rows along the grid
-  int splits;      // CTAs that share a unit's keys
-  float4 *part_o;  // splits > 1: [unit][split][row tile][D / 4][128 rows], unnormalised sums
-  float2 *part_ml; // [unit][split][row tile][128 rows]: reference (log2) and sum
+  int whole;       // units that one CTA takes whole; the keys of the others are shared by
+  int splits;      // so many CTAs
+  float4 *part_o;  // [unit - whole][split][row tile][D / 4][128 rows], unnormalised sums
+  float2 *part_ml; // [unit - whole][split][row tile][128 rows]: reference (log2) and sum
 };
 
 template <int D>
@@ -455,9 +456,10 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
   const int tid = threadIdx.x, warp = uniform(tid >> 5);
   constexpr uint32_t kCols = 512;
   // Blocks of later rows (more keys) come first; the sequences and heads of one block of rows are neighbours.
-  const int units = p.B * p.Hk, split = static_cast<int>(blockIdx.x) % P.splits, cta = static_cast<int>(blockIdx.x) / P.splits;
-  const int first_rb = P.row_blocks - 1 - cta / units;
-  const int s = cta % units / p.Hk, kvh = cta % units % p.Hk;
+  const int shared_at = static_cast<int>(blockIdx.x) - P.whole;  // this CTA among those that share
+  const int splits = shared_at < 0 ? 1 : P.splits, split = shared_at < 0 ? 0 : shared_at % splits;
+  const int unit = shared_at < 0 ? static_cast<int>(blockIdx.x) : P.whole + shared_at / splits;
+  const int heads = p.B * p.Hk, first_rb = P.row_blocks - 1 - unit / heads, s = unit % heads / p.Hk, kvh = unit % heads % p.Hk;
   if (tid == 0) {
     mbar_init(&S.q_full, 8);
     for (int i = 0; i < 2; ++i) {
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
   u.rows = any ? static_cast<int64_t>(u.q.len) * u.G : 0;
   u.row0 = static_cast<int64_t>(first_rb) * 2 * kRows;
   const int tiles = u.row0 < u.rows ? max(u.tiles(0), u.tiles(1)) : 0;
-  if (split * share_of(tiles, P.splits) >= tiles) {  // (no such rows, or nothing left for this split)
+  if (split * share_of(tiles, splits) >= tiles) {  // (no such rows, or nothing left for this split)
     pdl_launch_dependents();
     return;
   }
@@ -511,9 +513,9 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
       u.row0 = (first_rb + static_cast<int64_t>(turn) * P.row_blocks) * 2 * kRows;
       int T0 = uniform(u.tiles(0)), T1 = uniform(u.tiles(1));
       u.j0 = 0;
-      part = P.splits > 1 && turn == 0;
+      part = splits > 1 && turn == 0;
       if (part) {
-        const int share = share_of(max(T0, T1), P.splits);
+        const int share = share_of(max(T0, T1), splits);
         u.j0 = split * share;
         T0 = min(max(T0 - u.j0, 0), share);
         T1 = min(max(T1 - u.j0, 0), share);
@@ -530,7 +532,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
     int done = 0, n_units = 0;
     units_loop([&](int T0, int T1) {
       const int t = warp / 4;
-      const int64_t slot = part ? (static_cast<int64_t>(first_rb * units + cta % units) * P.splits + split) * 2 + t : 0;
+      const int64_t slot = part ? (static_cast<int64_t>(unit - P.whole) * splits + split) * 2 + t : 0;
       softmax_role<D>(p, S, u, tmem, t, t == 0 ? T0 : T1, kv, done, n_units, dead,
                       part ? P.part_o + slot * (D / 4 * kRows) : nullptr, part ? P.part_ml + slot * kRows : nullptr);
     });
@@ -567,12 +569,12 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
 template <int D>
 __global__ void __launch_bounds__(kRows) kv4_prompt_combine_kernel(const __grid_constant__ PromptParams P) {
   const Kv4AttnLaunch &p = P.a;
-  const int units = p.B * p.Hk, t = blockIdx.x & 1, unit = static_cast<int>(blockIdx.x >> 1), r = threadIdx.x;
-  const int rb = unit / units, s = unit % units / p.Hk, c0 = blockIdx.y * 32;
+  const int heads = p.B * p.Hk, t = blockIdx.x & 1, shared_at = static_cast<int>(blockIdx.x >> 1), r = threadIdx.x;
+  const int unit = P.whole + shared_at, rb = P.row_blocks - 1 - unit / heads, s = unit % heads / p.Hk, c0 = blockIdx.y * 32;
   // (this grid starts once every CTA of the first kernel is past its own wait: the lengths can be read)
   PromptUnit u;
   u.G = p.Hq / p.Hk;
-  u.kvh = unit % units % p.Hk;
+  u.kvh = unit % heads % p.Hk;
   const bool any = seq_info(p, s, &u.q, false);
   u.rows = any ? static_cast<int64_t>(u.q.len) * u.G : 0;
   u.row0 = static_cast<int64_t>(rb) * 2 * kRows;
@@ -586,7 +588,7 @@ __global__ void __launch_bounds__(kRows) kv4_prompt_combine_kernel(const __grid_
   pdl_launch_dependents();
   if (row >= u.rows) return;
   const int64_t index = (u.q.tok0 + row / u.G) * p.Hq + u.kvh * u.G + row % u.G;
-  const int64_t slot0 = static_cast<int64_t>(unit) * P.splits * 2 + t;
+  const int64_t slot0 = static_cast<int64_t>(shared_at) * P.splits * 2 + t;
   float top = -INFINITY;
   for (int k = 0; k < parts; ++k) top = fmaxf(top, P.part_ml[(slot0 + 2 * k) * kRows + r].x);
   float sum = 0.f, acc[32];
@@ -616,22 +618,25 @@ __global__ void __launch_bounds__(kRows) kv4_prompt_combine_kernel(const __grid_
 
 size_t part_rows(const Kv4AttnLaunch &p) {  // rows of all parts
   const Kv4PromptShape g = kv4_prompt_shape(p);
-  return g.splits == 1 ? 0 : static_cast<size_t>(g.row_blocks) * p.B * p.Hk * g.splits * 2 * kRows;
+  return (static_cast<size_t>(g.row_blocks) * p.B * p.Hk - g.whole) * g.splits * 2 * kRows;
 }
 
 template <int D>
 cudaError_t launch_typed(const PromptParams &P, cudaStream_t st) {
   const size_t smem = sizeof(PromptSmem<D>) + 1024;
-  const unsigned units = static_cast<unsigned>(P.row_blocks) * P.a.B * P.a.Hk;
-  const cudaError_t e = launch_large<kv4_prompt_kernel<D>>(dim3(units * P.splits), dim3(kPThreads), smem, st, P);
-  if (e != cudaSuccess || P.splits == 1) return e;
-  return launch_pdl(kv4_prompt_combine_kernel<D>, dim3(2 * units, D / 32), dim3(kRows), 0, st, 1, P);
+  const unsigned shared = static_cast<unsigned>(P.row_blocks) * P.a.B * P.a.Hk - P.whole;
+  const cudaError_t e = launch_large<kv4_prompt_kernel<D>>(dim3(P.whole + shared * P.splits), dim3(kPThreads), smem, st, P);
+  if (e != cudaSuccess || shared == 0) return e;
+  return launch_pdl(kv4_prompt_combine_kernel<D>, dim3(2 * shared, D / 32), dim3(kRows), 0, st, 1, P);
 }
 
 }  // namespace
 
-// Blocks of 256 rows of the longest sequence, and CTAs per block. With at most half as many blocks as SMs the keys are
-// split too (one wave of CTAs, four tiles of 128 keys each at least of the longest context that the table holds).
+// Blocks of 256 rows of the longest sequence, and how their keys are shared out. With at most half as many units (blocks x
+// key heads x sequences) as SMs every unit's keys go to as many CTAs as fit one wave, four tiles of 128 keys each at least of the
+// longest context that the table holds. With one to four waves of units the last, partial wave is shared by two to eight CTAs a
+// unit where that shortens it by an eighth of a unit or more (2048 tokens behind 14336, 256 units on 148 SMs, the last 108 by
+// four: see the measurement at the file's head).
 Kv4PromptShape kv4_prompt_shape(const Kv4AttnLaunch &p) {
   Kv4PromptShape g;
   const int64_t heads = static_cast<int64_t>(p.B) * p.Hk;
@@ -641,10 +646,22 @@ Kv4PromptShape kv4_prompt_shape(const Kv4AttnLaunch &p) {
   if (blocks > room) blocks = room;
   if (blocks < 1) blocks = 1;
   g.row_blocks = static_cast<int>(blocks);
-  const int64_t sms = sm_count(), tiles = static_cast<int64_t>(p.cache.max_blocks) * (DSV4_PAGE_POSITIONS / kKeys);
-  int64_t splits = sms / (blocks * heads);
-  if (splits > tiles / 4) splits = tiles / 4;
-  g.splits = splits < 2 ? 1 : static_cast<int>(splits);
+  const int64_t units = blocks * heads, sms = sm_count();
+  const int64_t tiles = static_cast<int64_t>(p.cache.max_blocks) * (DSV4_PAGE_POSITIONS / kKeys);
+  g.whole = static_cast<int>(units);
+  g.splits = 1;
+  if (2 * units <= sms) {
+    int64_t splits = sms / units;
+    if (splits > tiles / 4) splits = tiles / 4;
+    if (splits >= 2) g.whole = 0, g.splits = static_cast<int>(splits);
+  } else if (units > sms && units <= 4 * sms && units % sms != 0) {
+    const int64_t rest = units % sms;
+    double best = 1.0 - 0.125;
+    for (int k = 2; k <= 8 && k <= tiles / 8; ++k) {
+      const double time = static_cast<double>((rest * k + sms - 1) / sms) / k;
+      if (time < best) best = time, g.whole = static_cast<int>(units - rest), g.splits = k;
+    }
+  }
   return g;
 }
 
@@ -657,6 +674,7 @@ cudaError_t launch_kv4_prompt(const Kv4AttnLaunch &q, void *ws, cudaStream_t st)
   P.a = q;
   const Kv4PromptShape g = kv4_prompt_shape(q);
   P.row_blocks = g.row_blocks;
+  P.whole = g.whole;
   P.splits = g.splits;
   P.part_o = static_cast<float4 *>(ws);
   P.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(ws) + align_up(part_rows(q) * q.D * sizeof(float), 256));

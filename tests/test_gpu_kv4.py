@@ -350,7 +350,8 @@ def test_attention_of_many_sequences():
         check_attention(c, q, lens, starts, out, lse)
 
 
-@pytest.mark.parametrize("Hq,Hk,lens,starts", [(4, 1, [300], [9000]), (16, 2, [33, 1], [5000, 7000]), (8, 1, [700, 300], [3000, 0])])
+@pytest.mark.parametrize("Hq,Hk,lens,starts", [(4, 1, [300], [9000]), (16, 2, [33, 1], [5000, 7000]), (8, 1, [700, 300], [3000, 0]),
+                                               (80, 20, [300, 280], [2100, 0])])  # the last: more blocks than SMs, a partial wave
 def test_attention_splits_the_keys_of_few_rows(Hq, Hk, lens, starts):
     """Few blocks of rows over a long context: the keys are shared out; a hint that is too small leaves rows to walk on over."""
     require_gpu()
