@@ -45,7 +45,7 @@ constexpr int kTile = 64;       // keys of a warp's turn
 constexpr int kWarps = 4;
 constexpr int kThreadsA = 32 * kWarps;
 constexpr float kPOff = 14.f;   // weights are held times 2^14
-constexpr int kMinTiles = 4;    // tiles of a slice, at least (one per warp)
+constexpr int kMinKeysLog2 = 8; // keys of a slice, at least 256 (a tile for each warp)
 
 struct AttnParams {
   Kv4AttnLaunch a;
@@ -53,6 +53,7 @@ struct AttnParams {
   float2 *part_ml;   // [2 slots][R] per CTA: maximum (log2) and sum
   int ctas;
   int group;         // query heads of a key/value head
+  int key_log2;      // keys of a tile of the line: 64 or 128
 };
 
 // ---------------------------------------------------------------- the line of work
@@ -65,10 +66,11 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 struct Line {
   const Kv4AttnLaunch *p;
   int G, R, r_log2;  // rows of a tile: a power of two
+  int key_log2;      // keys of a tile
   __device__ __forceinline__ int row_tiles(const Seq &q) const {
     return static_cast<int>((static_cast<int64_t>(q.len) * G + R - 1) >> r_log2);
   }
-  __device__ __forceinline__ int tiles(const Seq &q) const { return (q.n + kTile - 1) / kTile; }
+  __device__ __forceinline__ int tiles(const Seq &q) const { return (q.n + (1 << key_log2) - 1) >> key_log2; }
   __device__ __forceinline__ int64_t weight(int s, bool tell = false) const {
     Seq q;
     if (!seq_info(*p, s, &q, tell)) return 0;
@@ -185,8 +187,9 @@ __device__ __forceinline__ int64_t slice_at(int64_t all, int ctas, int c) {
   const int64_t each = quotient(all, ctas);
   return each * c + quotient((all - each * ctas) * c, ctas);
 }
-__device__ __forceinline__ int slices(int64_t all, int ctas) {
-  const int64_t most = (all + kMinTiles - 1) / kMinTiles;  // (a shift)
+__device__ __forceinline__ int slices(int64_t all, int ctas, int key_log2) {
+  const int least_log2 = kMinKeysLog2 - key_log2;
+  const int64_t most = (all + (1 << least_log2) - 1) >> least_log2;
   return most < ctas ? static_cast<int>(most) : ctas;
 }
 
@@ -209,6 +212,13 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
+}
+
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 
 // Row of a 16-key group that fragment row g (0..7) stands for: neighbouring pairs differ in parity
@@ -248,6 +258,46 @@ struct alignas(128) AttnSmem {
   int abort_flag;
 };
 
+// The warps' sums of a unit's part together, by all 32 kWarps threads: to the output where the part is the whole unit.
+template <int D, int R, class Smem>
+__device__ __forceinline__ void join_part(const AttnParams &P, Smem &S, const Walk &w, int stop) {
+  const Kv4AttnLaunch &p = P.a;
+  const int tid = threadIdx.x;
+  const bool whole = w.tile == 0 && stop == w.tiles;
+  const int part = 2 * static_cast<int>(blockIdx.x) + (w.tile == 0 ? 1 : 0);
+  constexpr int V4 = D / 4;
+  for (int e = tid; e < R * V4; e += 32 * kWarps) {
+    const int r = e / V4, d = e % V4 * 4;
+    const int rl = S.lim[r];
+    if (rl == 0) continue;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) mx = fmaxf(mx, S.ml[k][r].x);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      const float2 ml = S.ml[k][r];
+      const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2_approx(ml.x - mx);
+      const float4 v = *reinterpret_cast<const float4 *>(&S.o[k][r][d]);
+      sum = fmaf(ml.y, f, sum);
+      acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
+      acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
+    }
+    if (S.nan_at[d / kKv4Block] < rl) acc.x = acc.y = acc.z = acc.w = __uint_as_float(0x7FC00000u);
+    if (whole) {
+      const int64_t row = S.index[r];
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const uint2 b = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+      *reinterpret_cast<uint2 *>(p.out + row * D + d) = b;
+      if (d == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (mx - kPOff + log2f(sum)) * 0.6931471805599453f;
+    } else {
+      *reinterpret_cast<float4 *>(P.part_o + (static_cast<int64_t>(part) * R + r) * D + d) = acc;
+      if (d == 0) P.part_ml[part * R + r] = make_float2(mx, sum);
+    }
+  }
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreadsA, StepShape<D, NT>::kResident)
     kv4_step_kernel(const __grid_constant__ AttnParams P) {
@@ -266,10 +316,10 @@ __global__ void __launch_bounds__(kThreadsA, StepShape<D, NT>::kResident)
   }
   pdl_wait();
   pdl_launch_dependents();
-  const Line line{&p, P.group, R, 31 - __clz(R)};
+  const Line line{&p, P.group, R, 31 - __clz(R), P.key_log2};
   const int chunk = (p.B + kThreadsA - 1) / kThreadsA;
   const int64_t all = line_prefix(line, kThreadsA, chunk, S.prefix, S.warp_sums);
-  const int ctas = slices(all, P.ctas);
+  const int ctas = slices(all, P.ctas, P.key_log2);
   if (static_cast<int>(blockIdx.x) >= ctas) return;
   const int64_t from = slice_at(all, ctas, blockIdx.x), to = slice_at(all, ctas, blockIdx.x + 1);
   Walk w;
@@ -361,9 +411,12 @@ __global__ void __launch_bounds__(kThreadsA, StepShape<D, NT>::kResident)
           const uint4 v = rl > 0 ? *reinterpret_cast<const uint4 *>(src + 8 * i) : make_uint4(0, 0, 0, 0);
           qf[nt][2 * i][0] = v.x, qf[nt][2 * i][1] = v.y, qf[nt][2 * i + 1][0] = v.z, qf[nt][2 * i + 1][1] = v.w;
         }
-        lim[nt][0] = __shfl_sync(0xFFFFFFFFu, my_lim, 8 * nt + 2 * t4);
-        lim[nt][1] = __shfl_sync(0xFFFFFFFFu, my_lim, 8 * nt + 2 * t4 + 1);
-        least = min(least, min(lim[nt][0], lim[nt][1]));
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int there = __shfl_sync(0xFFFFFFFFu, my_lim, 8 * nt + 2 * t4 + c);
+          lim[nt][c] = there > 0 ? there : limit;  // (a row that is not there needs no mask: its sums are not written)
+          least = min(least, lim[nt][c]);
+        }
       }
       if (first) fetch_first(w);
       first = false;
@@ -600,39 +653,7 @@ __global__ void __launch_bounds__(kThreadsA, StepShape<D, NT>::kResident)
         }
       }
       __syncthreads();
-      const bool whole = w.tile == 0 && stop == w.tiles;
-      const int part = 2 * static_cast<int>(blockIdx.x) + (w.tile == 0 ? 1 : 0);
-      constexpr int V4 = D / 4;
-      for (int e = tid; e < R * V4; e += 32 * kWarps) {
-        const int r = e / V4, d = e % V4 * 4;
-        const int rl = S.lim[r];
-        if (rl == 0) continue;
-        float mx = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) mx = fmaxf(mx, S.ml[k][r].x);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-          const float2 ml = S.ml[k][r];
-          const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2_approx(ml.x - mx);
-          const float4 v = *reinterpret_cast<const float4 *>(&S.o[k][r][d]);
-          sum = fmaf(ml.y, f, sum);
-          acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
-          acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
-        }
-        if (S.nan_at[d / kKv4Block] < rl) acc.x = acc.y = acc.z = acc.w = __uint_as_float(0x7FC00000u);
-        if (whole) {
-          const int64_t row = S.index[r];
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          const uint2 b = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-          *reinterpret_cast<uint2 *>(p.out + row * D + d) = b;
-          if (d == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (mx - kPOff + log2f(sum)) * 0.6931471805599453f;
-        } else {
-          *reinterpret_cast<float4 *>(P.part_o + (static_cast<int64_t>(part) * R + r) * D + d) = acc;
-          if (d == 0) P.part_ml[part * R + r] = make_float2(mx, sum);
-        }
-      }
+      join_part<D, R>(P, S, w, stop);
       __syncthreads();
       if (!more) break;
       w = nx;
@@ -644,6 +665,435 @@ __global__ void __launch_bounds__(kThreadsA, StepShape<D, NT>::kResident)
   if (S.abort_flag && lane == 0) report(p.d_status, DSV4_DEV_TIMEOUT);
 }
 
+// ---------------------------------------------------------------- few rows, long contexts: scores on the tensor cores
+
+// The same slices, in tiles of 128 keys, for at most 8 rows of 128 channels. The codes of K are an operand of
+// tcgen05.mma (kind::f8f6f4, e2m1) as they are: a block of 32 channels is one product of depth 32, keys on
+// the 128-row side, whose sums the block's scale multiplies afterwards:
+//   s_j = sum_b 2^k_jb (sum_c code_jc q_c)          8 x 4 scales a key in place of 128 conversions and products
+// q enters as two e4m3 values, hi + lo / 32, that hold its 8 bits exactly but for elements 2^-12 below the row's
+// largest, which are off by at most 2^-22 of that: columns 0-7 are the rows' hi and 8-15 their lo.
+// Warp 4 brings keys (TMA, which spreads the codes to the operand's layout) and values (bulk copies) into two stages
+// each and issues the products; warps 0-3 take 32 keys of each tile, one per lane: scales, weights, and P to shared
+// memory, from where it is the B operand of mma.sync with the values as in the kernel above.
+// The reference of the weights is an integer (so that taking it off twice rounds alike), raised when a score exceeds
+// it by more than 2^8; weights are held times 2^7.
+constexpr int kTcKeys = 128;
+constexpr int kTcThreads = 32 * (kWarps + 1);
+constexpr int kTcResident = 3;
+constexpr int kTcCols = 128;       // TMEM columns: two tiles of 4 blocks x 16
+constexpr float kTcOff = 7.f;      // weights are held times 2^7
+constexpr float kTcRaise = 8.f;
+constexpr float kTcNone = 3e38f;   // off of a row without a reference yet
+
+struct alignas(1024) TcStepSmem {
+  uint8_t k[2][kTcKeys * 128];     // codes, spread: 16 of them in each 16 bytes
+  uint8_t q[16 * 128];             // e4m3: rows 0-7 hi, 8-15 lo
+  struct alignas(128) Values {
+    uint8_t c[kTcKeys * 64], ks[kTcKeys * 4], vs[kTcKeys * 4];
+  } v[2];
+  uint4 pw[kWarps][32];            // weights of a warp's keys, fp16
+  float o[kWarps][8][128 + 4];
+  float2 ml[kWarps][8];
+  float keep[kWarps][8];
+  alignas(16) float rs[8];         // log2 score per product
+  alignas(16) int lim[8];
+  int64_t index[8];
+  int64_t prefix[kTcThreads + 1], warp_sums[kTcThreads / 32];
+  uint64_t k_full[2], v_full[2], v_free[2], s_full[2], s_free[2], q_full;
+  int bad[2];
+  int nan_at[128 / kKv4Block];
+  int abort_flag;
+  uint32_t tmem_base;
+};
+
+__device__ __forceinline__ int tc_seen(const Walk &u) {
+  return max(min(u.stop(), (u.unit_limit() + kTcKeys - 1) / kTcKeys) - u.tile, 0);
+}
+
+// copies and products of the slice; w at its start
+__device__ __forceinline__ void tc_feed(const AttnParams &P, const CUtensorMap &map, TcStepSmem &S, Walk &w, uint32_t tmem) {
+  const Kv4AttnLaunch &p = P.a;
+  const int lane = threadIdx.x & 31;
+  struct Tile {
+    int row;      // of the cache; negative: the page does not exist
+    bool first;   // of its unit
+  };
+  int i = 0, count = tc_seen(w);
+  bool fresh = true;
+  auto settle = [&]() -> bool {  // the next unit with tiles, where this one has none left
+    while (i >= count) {
+      if (!w.next()) return false;
+      i = 0;
+      count = tc_seen(w);
+      fresh = true;
+    }
+    return true;
+  };
+  auto look = [&]() -> Tile {
+    const int t = w.tile + i;
+    const int page = p.cache.block_table[static_cast<int64_t>(w.s) * p.cache.max_blocks + t / (DSV4_PAGE_POSITIONS / kTcKeys)];
+    Tile c;
+    c.first = fresh;
+    if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.cache.num_pages)) {
+      c.row = -1;
+      if (lane == 0) report(p.d_status, DSV4_DEV_BAD_PAGE);
+    } else {
+      c.row = (page * p.Hk + w.kvh) * DSV4_PAGE_POSITIONS + t % (DSV4_PAGE_POSITIONS / kTcKeys) * kTcKeys;
+    }
+    fresh = false;
+    ++i;
+    return c;
+  };
+  bool dead = false;
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (!dead) dead = !__all_sync(0xFFFFFFFFu, mbar_spin(bar, parity & 1, &S.abort_flag));
+  };
+  auto load_k = [&](uint32_t n, const Tile &c) {
+    if (lane != 0) return;
+    uint64_t *bar = &S.k_full[n & 1];
+    if (c.row < 0) {
+      mbar_arrive(bar);
+    } else {  // (the transaction counts the packed bytes)
+      mbar_arrive_expect_tx(bar, kTcKeys * 64);
+      tma_load_2d(S.k[n & 1], &map, bar, 0, c.row);
+    }
+  };
+  auto load_v = [&](uint32_t n, const Tile &c) {
+    if (lane != 0) return;
+    uint64_t *bar = &S.v_full[n & 1];
+    S.bad[n & 1] = c.row < 0;
+    if (c.row < 0) {
+      mbar_arrive(bar);
+    } else {
+      TcStepSmem::Values &T = S.v[n & 1];
+      const int64_t row = c.row;
+      mbar_arrive_expect_tx(bar, kTcKeys * (64 + 4 + 4));
+      bulk_load(T.ks, p.cache.k_scales + row * 4, kTcKeys * 4, bar);
+      bulk_load(T.c, p.cache.v_codes + row * 64, kTcKeys * 64, bar);
+      bulk_load(T.vs, p.cache.v_scales + row * 4, kTcKeys * 4, bar);
+    }
+  };
+  constexpr uint32_t id = idesc_e2m1_e4m3(kTcKeys, 16);
+  const uint64_t qd = sw128_desc(smem_u32(S.q), 16, 1024);
+  uint32_t n = 0, loaded_k = 0, loaded_v = 0, units = 0;
+  bool have = settle();
+  Tile cur{}, nxt{};
+  if (have) {
+    cur = look();
+    load_k(loaded_k++, cur);
+  }
+  for (; have; ++n) {
+    const bool more = settle();
+    if (more) {
+      nxt = look();
+      if (n >= 1) wait(&S.s_full[(n - 1) & 1], (n - 1) >> 1);  // its stage's products are done
+      if (dead) break;
+      load_k(loaded_k++, nxt);
+    }
+    if (n >= 2) wait(&S.v_free[n & 1], (n >> 1) - 1);
+    if (dead) break;
+    load_v(loaded_v++, cur);
+    if (cur.first) wait(&S.q_full, units++);
+    wait(&S.k_full[n & 1], n >> 1);
+    if (n >= 2) wait(&S.s_free[n & 1], (n >> 1) - 1);
+    if (dead) break;
+    tc_fence_after();
+    const uint64_t kd = sw128_desc(smem_u32(S.k[n & 1]), 16, 1024);
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      if (elect_one()) mma_e4m3(tmem + 64 * (n & 1) + 16 * b, kd + 2 * b, qd + 2 * b, id, 0);
+    if (elect_one()) mma_commit(&S.s_full[n & 1]);
+    cur = nxt;
+    have = more;
+  }
+  if (dead) {  // let what is in flight land before the CTA leaves
+    volatile int dummy = 0;
+    for (uint32_t j = loaded_k < 2 ? 0 : loaded_k - 2; j < loaded_k; ++j) mbar_wait(&S.k_full[j & 1], (j >> 1) & 1, &dummy);
+    for (uint32_t j = loaded_v < 2 ? 0 : loaded_v - 2; j < loaded_v; ++j) mbar_wait(&S.v_full[j & 1], (j >> 1) & 1, &dummy);
+    for (uint32_t j = n < 2 ? 0 : n - 2; j < n; ++j) mbar_wait(&S.s_full[j & 1], (j >> 1) & 1, &dummy);
+  }
+}
+
+// softmax and values of the slice, warps 0-3
+__device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Walk &w, uint32_t tmem) {
+  constexpr int D = 128, R = 8, KS = D / 16;
+  const Kv4AttnLaunch &p = P.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t4 = lane & 3;
+  const uint32_t pw_at = smem_u32(&S.pw[warp][8 * (lane >> 3) + key_of(lane & 7)]);
+  uint32_t n = 0;  // tiles of the CTA
+  bool dead = false;
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (!dead) dead = !__all_sync(0xFFFFFFFFu, mbar_spin(bar, parity & 1, &S.abort_flag));
+  };
+  for (;;) {
+    const int stop = w.stop(), limit = w.unit_limit(), count = tc_seen(w);
+    {  // thread: channels 8 (tid % 16) .. of row tid / 16
+      const int r = tid >> 4, c = tid & 15;
+      const int64_t row = static_cast<int64_t>(w.rt) * R + r, G = w.ln.G;
+      const bool there = row < static_cast<int64_t>(w.q.len) * G;
+      const int64_t i = there ? quotient(row, G) : 0, tok = w.q.tok0 + i;
+      const int64_t head = w.kvh * G + (row - i * G);
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (there) v = *reinterpret_cast<const uint4 *>(p.q + tok * p.q_stride + head * D + 8 * c);
+      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+      uint32_t am = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) am = max(am, max((x[k] << 16) & 0x7FFF0000u, x[k] & 0x7FFF0000u));
+#pragma unroll
+      for (int o2 = 1; o2 < 16; o2 <<= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, o2));
+      // 2^sh brings the largest element to [2^7, 2^8); a row with an infinity or NaN has no finite score
+      const int ex = static_cast<int>(am >> 23) - 127;
+      const int sh = (am == 0 || ex >= 128) ? 0 : min(max(7 - ex, -120), 120);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float a = __uint_as_float(x[k] << 16) * up, b = __uint_as_float(x[k] & 0xFFFF0000u) * up;
+        float ha, hb;
+        hi[k] = e4m3_pair(a, b, ha, hb);
+        float la, lb;
+        lo[k] = e4m3_pair((a - ha) * 32.f, (b - hb) * 32.f, la, lb);
+      }
+      const uint32_t at = sw128_offset(r, c >> 1) + 8 * (c & 1);
+      *reinterpret_cast<uint2 *>(S.q + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+      *reinterpret_cast<uint2 *>(S.q + 1024 + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+      if (c == 0) {
+        S.lim[r] = there ? min(w.q.n, w.q.start + static_cast<int>(i) + 1) : 0;
+        S.index[r] = tok * p.Hq + head;
+        S.rs[r] = ex >= 128 ? __uint_as_float(0x7FC00000u)
+                            : p.softmax_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+      }
+      if (tid < D / kKv4Block) S.nan_at[tid] = 0x7FFFFFFF;
+    }
+    fence_proxy_async_smem();
+    named_bar_sync(1, 32 * kWarps);
+    if (count > 0 && lane == 0) mbar_arrive(&S.q_full);
+    int least = limit;  // positions that every row sees
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int x = S.lim[r];
+      if (x > 0) least = min(least, x);
+    }
+    float o[KS][4];
+    uint64_t off[R / 2], l[R / 2];  // per pair of rows: kTcOff - reference; this lane's sums
+#pragma unroll
+    for (int k = 0; k < KS; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < R / 2; ++k) off[k] = pack_f32x2(kTcNone, kTcNone), l[k] = 0;
+
+    for (int i = 0; i < count; ++i, ++n) {
+      const uint32_t slot = n & 1;
+      wait(&S.v_full[slot], n >> 1);
+      wait(&S.s_full[slot], n >> 1);
+      if (dead) break;
+      tc_fence_after();
+      const TcStepSmem::Values &T = S.v[slot];
+      const bool bad = S.bad[slot];
+      const int key0 = (w.tile + i) * kTcKeys + 32 * warp;  // the warp's first key
+      const bool edge = key0 + 32 > least;
+      const uint32_t kb = *reinterpret_cast<const uint32_t *>(T.ks + 4 * (32 * warp + lane));
+      const uint32_t s_at = tmem + 64 * slot + (static_cast<uint32_t>(32 * warp) << 16);
+      uint64_t s[R / 2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t a[32];
+        tmem_ld32(s_at + 32 * h, a);
+        tmem_ld_wait();
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const float f = scale_value(kb >> (8 * (2 * h + b)) & 255u);
+          const uint64_t f2 = pack_f32x2(f, f), part = pack_f32x2(0.03125f, 0.03125f);
+#pragma unroll
+          for (int k = 0; k < R / 2; ++k) {
+            const uint64_t hi = pack_f32x2(__uint_as_float(a[16 * b + 2 * k]), __uint_as_float(a[16 * b + 2 * k + 1]));
+            const uint64_t lo = pack_f32x2(__uint_as_float(a[16 * b + 8 + 2 * k]), __uint_as_float(a[16 * b + 9 + 2 * k]));
+            const uint64_t x = fma_f32x2(lo, part, hi);
+            s[k] = h + b == 0 ? mul_f32x2(f2, x) : fma_f32x2(f2, x, s[k]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.s_free[slot]);
+      if (edge || bad) {
+#pragma unroll
+        for (int k = 0; k < R / 2; ++k) {
+          float a, b;
+          unpack_f32x2(s[k], a, b);
+          // (a row that is not there needs no mask, but for positions behind the last: its sums are not written)
+          const int la = S.lim[2 * k], lb = S.lim[2 * k + 1];
+          if (bad || key0 + lane >= (la > 0 ? la : limit)) a = -INFINITY;
+          if (bad || key0 + lane >= (lb > 0 ? lb : limit)) b = -INFINITY;
+          s[k] = pack_f32x2(a, b);
+        }
+      }
+      uint64_t rs[R / 2];
+#pragma unroll
+      for (int k = 0; k < R / 2; ++k) rs[k] = *reinterpret_cast<const uint64_t *>(&S.rs[2 * k]);
+      float y[R];
+      float most = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < R / 2; ++k) {
+        unpack_f32x2(fma_f32x2(s[k], rs[k], off[k]), y[2 * k], y[2 * k + 1]);
+        most = fmaxf(most, fmaxf(y[2 * k], y[2 * k + 1]));
+      }
+      if (__any_sync(0xFFFFFFFFu, most > kTcOff + kTcRaise)) {
+#pragma unroll
+        for (int k = 0; k < R / 2; ++k) {
+          float x[2], f[2], sums[2];
+          unpack_f32x2(mul_f32x2(s[k], rs[k]), x[0], x[1]);
+          unpack_f32x2(off[k], f[0], f[1]);
+          unpack_f32x2(l[k], sums[0], sums[1]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int o2 = 1; o2 < 32; o2 <<= 1) x[c] = fmaxf(x[c], __shfl_xor_sync(0xFFFFFFFFu, x[c], o2));
+            const float was = f[c] == kTcNone ? -kTcNone : kTcOff - f[c], now = fmaxf(was, ceilf(x[c]));
+            const float keep = now == was ? 1.f : ex2_approx(was - now);
+            if (now != was) f[c] = kTcOff - now;
+            sums[c] *= keep;
+            if (lane == 0) S.keep[warp][2 * k + c] = keep;
+          }
+          off[k] = pack_f32x2(f[0], f[1]);
+          l[k] = pack_f32x2(sums[0], sums[1]);
+          unpack_f32x2(fma_f32x2(s[k], rs[k], off[k]), y[2 * k], y[2 * k + 1]);
+        }
+        __syncwarp();
+        const float2 keep = *reinterpret_cast<const float2 *>(&S.keep[warp][2 * t4]);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) o[k][0] *= keep.x, o[k][1] *= keep.y, o[k][2] *= keep.x, o[k][3] *= keep.y;
+        __syncwarp();
+      }
+      uint32_t h[R / 2];
+#pragma unroll
+      for (int k = 0; k < R / 2; ++k) {
+        const float a = ex2_approx(y[2 * k]), b = ex2_approx(y[2 * k + 1]);
+        l[k] = add_f32x2(l[k], pack_f32x2(a, b));
+        h[k] = pack_half2(a, b);
+      }
+      S.pw[warp][lane] = make_uint4(h[0], h[1], h[2], h[3]);
+      __syncwarp();
+      uint32_t pb[4];
+      ldmatrix4_trans(pb, pw_at);
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const int kA = 16 * mt + key_of(2 * t4), kB = 16 * mt + key_of(2 * t4 + 1);  // of the warp's 32
+        uint32_t c4[4][2];
+        float sf[4];
+        const int blk = g >> 1;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int key = 32 * warp + ((q & 1) ? kB : kA) + (q >> 1) * 8;
+          const uint2 v = *reinterpret_cast<const uint2 *>(T.c + key * 64 + g * 8);
+          c4[q][0] = v.x, c4[q][1] = v.y;
+          sf[q] = __uint_as_float(static_cast<uint32_t>(T.vs[key * 4 + blk]) << 23);
+        }
+        if (edge || bad) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)  // not a position of the unit
+            if (bad || key0 + ((q & 1) ? kB : kA) + (q >> 1) * 8 >= limit) sf[q] = 0.f;
+        }
+        if ((sf[0] + sf[1]) + (sf[2] + sf[3]) == INFINITY) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (sf[q] == INFINITY) {
+              atomicMin(&S.nan_at[blk], key0 + ((q & 1) ? kB : kA) + (q >> 1) * 8);
+              sf[q] = 0.f;
+            }
+        }
+        const uint32_t sAB = pack_half2(sf[0], sf[1]), sCD = pack_half2(sf[2], sf[3]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t lo[2][4], hi[2][4];  // as in the kernel above
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t x = c4[2 * q][c], z = c4[2 * q + 1][c];
+            e2m1x8_to_half2((x & 0x0F0F0F0Fu) | (z << 4 & 0xF0F0F0F0u), lo[q]);
+            e2m1x8_to_half2((x >> 4 & 0x0F0F0F0Fu) | (z & 0xF0F0F0F0u), hi[q]);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma16816(o[4 * c + k], hmul2(lo[0][k], sAB), hmul2(hi[0][k], sAB), hmul2(lo[1][k], sCD), hmul2(hi[1][k], sCD),
+                     pb[2 * mt], pb[2 * mt + 1]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.v_free[slot]);
+    }
+#pragma unroll
+    for (int k = 0; k < R / 2; ++k) {
+      float f[2], sums[2];
+      unpack_f32x2(off[k], f[0], f[1]);
+      unpack_f32x2(l[k], sums[0], sums[1]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int o2 = 1; o2 < 32; o2 <<= 1) sums[c] += __shfl_xor_sync(0xFFFFFFFFu, sums[c], o2);
+        // as a reference for weights times 2^kPOff
+        if (lane == 0) S.ml[warp][2 * k + c] = make_float2(f[c] == kTcNone ? -INFINITY : kPOff - f[c], sums[c]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+        *reinterpret_cast<float2 *>(&S.o[warp][2 * t4 + c][16 * g + 2 * k]) = make_float2(o[k][c], o[k][2 + c]);
+    named_bar_sync(1, 32 * kWarps);
+    join_part<D, R>(P, S, w, stop);
+    named_bar_sync(1, 32 * kWarps);
+    if (!w.next()) break;
+  }
+}
+
+__global__ void __launch_bounds__(kTcThreads, kTcResident)
+    kv4_step_tc_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ CUtensorMap map) {
+  extern __shared__ uint8_t smem_raw[];
+  TcStepSmem &S = *reinterpret_cast<TcStepSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const Kv4AttnLaunch &p = P.a;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.k_full[i], 1);
+      mbar_init(&S.v_full[i], 1);
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.v_free[i], kWarps);
+      mbar_init(&S.s_free[i], kWarps);
+    }
+    mbar_init(&S.q_full, kWarps);
+    S.abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&map);
+  }
+  pdl_wait();
+  // (between the two: a kernel that this one waits for, or that waits for this one, may want all of TMEM)
+  if (warp == kWarps) {
+    tmem_alloc(&S.tmem_base, kTcCols);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  const Line line{&p, P.group, 8, 3, P.key_log2};
+  const int chunk = (p.B + kTcThreads - 1) / kTcThreads;
+  const int64_t all = line_prefix(line, kTcThreads, chunk, S.prefix, S.warp_sums);
+  tc_fence_after();
+  pdl_launch_dependents();
+  const uint32_t tmem = __reduce_max_sync(0xFFFFFFFFu, S.tmem_base);
+  const int ctas = slices(all, P.ctas, P.key_log2);
+  if (static_cast<int>(blockIdx.x) < ctas) {
+    Walk w;
+    w.begin(line, S.prefix, kTcThreads, chunk, slice_at(all, ctas, blockIdx.x), slice_at(all, ctas, blockIdx.x + 1));
+    fence_proxy_async_global();  // the cache's rows may come from the kernel before, by plain stores
+    if (warp == kWarps) tc_feed(P, map, S, w, tmem);
+    else tc_attend(P, S, w, tmem);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarps) tmem_dealloc(tmem, kTcCols);
+  if (S.abort_flag && tid == 0) report(p.d_status, DSV4_DEV_TIMEOUT);
+}
+
 // Joins the parts of a unit that several slices share: CTA c takes the unit that slice c starts
 // inside of, if no earlier slice does.
 constexpr int kCombineThreads = 128;
@@ -653,10 +1103,10 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const __gr
   const Kv4AttnLaunch &p = P.a;
   // (this grid starts once every CTA of the step kernel is past its own wait, so the lengths, which the
   // step kernel does not write, can be read before this one's)
-  const Line line{&p, P.group, R, 31 - __clz(R)};
+  const Line line{&p, P.group, R, 31 - __clz(R), P.key_log2};
   const int chunk = (p.B + kCombineThreads - 1) / kCombineThreads;
   const int64_t all = line_prefix(line, kCombineThreads, chunk, prefix, warp_sums);
-  const int ctas = slices(all, P.ctas);
+  const int ctas = slices(all, P.ctas, P.key_log2);
   const int c = static_cast<int>(blockIdx.x) + 1;
   Walk w;
   bool mine = c < ctas;
@@ -751,6 +1201,28 @@ cudaError_t launch_step(AttnParams &P, cudaStream_t st) {
   return launch_pdl(kv4_combine_kernel<D>, dim3(P.ctas - 1), dim3(kCombineThreads), 0, st, 1, P, 8 * NT);
 }
 
+// The form with scores on the tensor cores: its tensor map wants the codes at a multiple of 32 bytes and rows that
+// an int counts.
+bool make_codes_map(CUtensorMap *map, const Kv4AttnLaunch &p) {
+  const int64_t rows = static_cast<int64_t>(p.cache.num_pages) * p.Hk * DSV4_PAGE_POSITIONS;
+  if (rows > 0x7FFFFFFF || reinterpret_cast<uintptr_t>(p.cache.k_codes) % 32 != 0) return false;
+  auto fn = get_encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(rows)};  // codes
+  const cuuint64_t strides[1] = {64};                               // bytes
+  const cuuint32_t box[2] = {128, kTcKeys}, steps[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, p.cache.k_codes, dims, strides, box, steps,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_tc_step(AttnParams &P, const CUtensorMap &map, cudaStream_t st) {
+  const cudaError_t e =
+      launch_large<kv4_step_tc_kernel>(dim3(P.ctas), dim3(kTcThreads), sizeof(TcStepSmem) + 1024, st, P, map);
+  if (e != cudaSuccess || P.ctas == 1) return e;
+  return launch_pdl(kv4_combine_kernel<128>, dim3(P.ctas - 1), dim3(kCombineThreads), 0, st, 1, P, 8);
+}
+
 }  // namespace
 
 size_t kv4_attention_workspace_bytes(const Kv4AttnLaunch &p) {
@@ -765,11 +1237,15 @@ cudaError_t launch_kv4_attention(const Kv4AttnLaunch &q, void *ws, cudaStream_t 
   AttnParams P{};
   P.a = q;
   const int R = tile_rows(q);
-  P.ctas = sm_count() * resident(q);
+  CUtensorMap map;
+  const bool tc = q.D == 128 && R == 8 && make_codes_map(&map, q);
+  P.ctas = sm_count() * (tc ? kTcResident : resident(q));
+  P.key_log2 = tc ? 7 : 6;
   P.group = q.Hq / q.Hk;
   P.part_o = static_cast<float *>(ws);
   P.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(ws) +
                                          align_up(static_cast<size_t>(P.ctas) * 2 * R * q.D * sizeof(float), 256));
+  if (tc) return launch_tc_step(P, map, st);
   if (q.D == 64) return R == 8 ? launch_step<64, 1>(P, st) : launch_step<64, 2>(P, st);
   return R == 8 ? launch_step<128, 1>(P, st) : launch_step<128, 2>(P, st);
 }

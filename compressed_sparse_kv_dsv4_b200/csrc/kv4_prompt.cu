@@ -54,16 +54,6 @@ struct alignas(1024) PromptSmem {
   int nan_at[D / kKv4Block];   // smallest position with a NaN value block
 };
 
-// One lane of the warp. Through elect.sync the compiler knows that a single thread is inside the branch
-// and issues a product in few instructions; with "lane 0" as the condition (branch or predicate) an
-// issue took 75 to 170 cycles beside busy warps, more than the 64 that the product itself takes, with
-// elect.sync around each instruction 40 to 55.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t e;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-  return e != 0;
-}
-
 // tcgen05.mma kind::f16, A and B in shared memory (descriptors that share their high word) or A in TMEM
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t acc) {
   asm volatile(
