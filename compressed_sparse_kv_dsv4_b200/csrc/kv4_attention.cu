@@ -438,7 +438,9 @@ __global__ void __launch_bounds__(kThreadsA, StepShape<D, NT>::kResident)
           const uint32_t h = pack_half2(__uint_as_float(raw << 16) * up, __uint_as_float(raw & 0xFFFF0000u) * up);
           if (warp == 0) *reinterpret_cast<uint32_t *>(&S.q[8 * nt + g][8 * i + 2 * t4]) = h;
         }
-        const float mine = p.softmax_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+        // (not below float32's normal numbers: a masked position is minus infinity times this)
+        const float mine = fmaxf(
+            p.softmax_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23), 1.17549435e-38f);
         rs[nt][0] = __shfl_sync(0xFFFFFFFFu, mine, 8 * t4);      // lane 4 * (2 t4): column 2 t4
         rs[nt][1] = __shfl_sync(0xFFFFFFFFu, mine, 8 * t4 + 4);
       }
@@ -671,7 +673,7 @@ __global__ void __launch_bounds__(kThreadsA, StepShape<D, NT>::kResident)
 // tcgen05.mma (kind::f8f6f4, e2m1) as they are: a block of 32 channels is one product of depth 32, keys on
 // the 128-row side, whose sums the block's scale multiplies afterwards:
 //   s_j = sum_b 2^k_jb (sum_c code_jc q_c)          8 x 4 scales a key in place of 128 conversions and products
-// q enters as two e4m3 values, hi + lo / 32, that hold its 8 bits exactly but for elements 2^-12 below the row's
+// q enters as two e4m3 values, hi + lo / 32, that hold its 8 bits exactly but for elements 2^-14 below the row's
 // largest, which are off by at most 2^-22 of that: columns 0-7 are the rows' hi and 8-15 their lo.
 // Warp 4 brings keys (TMA, which spreads the codes to the operand's layout) and values (bulk copies) into two stages
 // each and issues the products; warps 0-3 take 32 keys of each tile, one per lane: scales, weights, and P to shared
@@ -863,7 +865,8 @@ __device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Wa
         S.lim[r] = there ? min(w.q.n, w.q.start + static_cast<int>(i) + 1) : 0;
         S.index[r] = tok * p.Hq + head;
         S.rs[r] = ex >= 128 ? __uint_as_float(0x7FC00000u)
-                            : p.softmax_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+                            : fmaxf(p.softmax_scale * 1.4426950408889634f *
+                                        __uint_as_float(static_cast<uint32_t>(127 - sh) << 23), 1.17549435e-38f);
       }
       if (tid < D / kKv4Block) S.nan_at[tid] = 0x7FFFFFFF;
     }
@@ -1094,8 +1097,10 @@ __global__ void __launch_bounds__(kTcThreads, kTcResident)
   if (S.abort_flag && tid == 0) report(p.d_status, DSV4_DEV_TIMEOUT);
 }
 
-// Joins the parts of a unit that several slices share: CTA c takes the unit that slice c starts
-// inside of, if no earlier slice does.
+// Joins the parts of a unit that several slices share. All slices but the first of a unit start inside it: their
+// CTAs here share its sums out, and the lanes of a CTA the parts of a sum, in an order that the number of slices fixes.
+// (With one CTA joining a unit, a call for one sequence of 32000 positions, 74 slices to each of 8 units, took 35.4 us;
+// so it takes 20.7 us. One of 131000: 59 us and 46 us.)
 constexpr int kCombineThreads = 128;
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const __grid_constant__ AttnParams P, int R) {
@@ -1110,31 +1115,44 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const __gr
   const int c = static_cast<int>(blockIdx.x) + 1;
   Walk w;
   bool mine = c < ctas;
-  int last = c;
+  int first = c, last = c;
   if (mine) {
     const int64_t from = slice_at(all, ctas, c);
     w.begin(line, prefix, kCombineThreads, chunk, from, from + 1);
-    const int64_t unit = from - w.tile;
-    mine = w.tile != 0 && slice_at(all, ctas, c - 1) <= unit;
-    if (mine)
-      while (last + 1 < ctas && slice_at(all, ctas, last + 1) < unit + w.tiles) ++last;
+    mine = w.tile != 0;
+    auto slice_of = [&](int64_t x) {  // the slice that x lies in
+      int k = min(static_cast<int>(static_cast<float>(x) / static_cast<float>(all) * ctas), ctas - 1);
+      while (slice_at(all, ctas, k) > x) --k;
+      while (slice_at(all, ctas, k + 1) <= x) ++k;
+      return k;
+    };
+    if (mine) {
+      first = slice_of(from - w.tile);
+      last = slice_of(from - w.tile + w.tiles - 1);
+    }
   }
   pdl_wait();
   pdl_launch_dependents();
   if (!mine) return;
   constexpr int V4 = D / 4, kAtOnce = 8;
-  for (int e = threadIdx.x; e < R * V4; e += kCombineThreads) {
+  const int parts = last - first + 1, rank = c - first - 1;
+  const int e0 = R * V4 * rank / (parts - 1), e1 = R * V4 * (rank + 1) / (parts - 1);
+  int lanes = 1;  // of a sum
+  while (lanes < 32 && 2 * lanes <= parts && kCombineThreads / (2 * lanes) >= e1 - e0) lanes *= 2;
+  const int mine_at = threadIdx.x & (lanes - 1), lanes_log2 = 31 - __clz(lanes);
+  for (int eb = e0; eb < e1; eb += kCombineThreads >> lanes_log2) {
+    const int e = eb + static_cast<int>(threadIdx.x >> lanes_log2);
     const int r = e / V4, d = e % V4 * 4;
-    if (w.row_limit(r) == 0) continue;
+    const bool there = e < e1 && w.row_limit(r) > 0;
     float mx = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = c - 1; k0 <= last; k0 += kAtOnce) {  // eight parts' loads at a time
+    for (int k0 = first + mine_at; there && k0 <= last; k0 += kAtOnce * lanes) {  // eight parts' loads at a time
       float2 ml[kAtOnce];
       float4 v[kAtOnce];
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
-        const int k = k0 + i;
-        const int64_t slot = 2 * k + (k == c - 1);
+        const int k = k0 + i * lanes;
+        const int64_t slot = 2 * k + (k == first);
         ml[i] = k <= last ? P.part_ml[slot * R + r] : make_float2(-INFINITY, 0.f);
         v[i] = k <= last ? *reinterpret_cast<const float4 *>(P.part_o + (slot * R + r) * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
@@ -1152,6 +1170,17 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const __gr
         acc.z = fmaf(v[i].z, f, acc.z), acc.w = fmaf(v[i].w, f, acc.w);
       }
     }
+    for (int o = 1; o < lanes; o <<= 1) {
+      const float mx2 = __shfl_xor_sync(0xFFFFFFFFu, mx, o), now = fmaxf(mx, mx2);
+      const float f = mx == -INFINITY && sum == 0.f ? 0.f : ex2_approx(mx - now);
+      auto add = [&](float x) {  // both sides' terms, each times its factor: the same sum on both
+        x *= f;
+        return x + __shfl_xor_sync(0xFFFFFFFFu, x, o);
+      };
+      sum = add(sum), acc.x = add(acc.x), acc.y = add(acc.y), acc.z = add(acc.z), acc.w = add(acc.w);
+      mx = now;
+    }
+    if (!there || mine_at != 0) continue;
     const int64_t row = w.row_index(r);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     *reinterpret_cast<uint2 *>(p.out + row * D + d) =
@@ -1184,12 +1213,14 @@ bool prompt_rows(const Kv4AttnLaunch &p) {
 // each of the SMs' twelve warps, going by the longest context that the table holds, 8 it is (16 rows over 4096
 // positions of one sequence 22 us against 29 us, over 32768 of eight 146 us against 114 us). Tiles of 32 rows at 64
 // channels were slower yet: 43.5 us against 34.5 us for 13 sequences of 20 rows and up to 9001 tokens.
-int tile_rows(const Kv4AttnLaunch &p) {
+int64_t turns_of_8(const Kv4AttnLaunch &p) {
   const int64_t group = p.Hq / p.Hk, rows = (p.max_new < p.T ? p.max_new : p.T) * group;
-  if (rows <= 8) return 8;
   const int64_t by_max = p.B * ((rows + 7) / 8), by_all = p.T * group / 8 + p.B;
-  const int64_t turns = p.Hk * (by_max < by_all ? by_max : by_all) * p.cache.max_blocks * (DSV4_PAGE_POSITIONS / kTile);
-  return turns < int64_t(8) * 12 * sm_count() ? 8 : 16;
+  return p.Hk * (by_max < by_all ? by_max : by_all) * p.cache.max_blocks * (DSV4_PAGE_POSITIONS / kTile);
+}
+int tile_rows(const Kv4AttnLaunch &p) {
+  const int64_t rows = (p.max_new < p.T ? p.max_new : p.T) * (p.Hq / p.Hk);
+  return rows <= 8 || turns_of_8(p) < int64_t(8) * 12 * sm_count() ? 8 : 16;
 }
 int resident(const Kv4AttnLaunch &p) { return resident_ctas(p.D, tile_rows(p) / 8); }
 
@@ -1201,7 +1232,16 @@ cudaError_t launch_step(AttnParams &P, cudaStream_t st) {
   return launch_pdl(kv4_combine_kernel<D>, dim3(P.ctas - 1), dim3(kCombineThreads), 0, st, 1, P, 8 * NT);
 }
 
-// The form with scores on the tensor cores: its tensor map wants the codes at a multiple of 32 bytes and rows that
+// The form with scores on the tensor cores takes calls of at least four of its tiles for each of its CTAs, going by the
+// longest context that the table holds; with fewer its start and its longer turns show. At 8 key heads of 8 query
+// heads each, the kernel above and this one: 8 sequences of 2000 positions (1024 tiles) 16.6 us and 20.6 us, one of
+// 32000 (2000) 22.0 us and 24.7 us; 64 of 500 (2048) 35.1 us and 27.8 us, 8 of 8000 (4096) 37.7 us and 30.4 us, 8 of
+// 32000 89.3 us and 74.5 us.
+bool tensor_scores(const Kv4AttnLaunch &p) {
+  return p.D == 128 && tile_rows(p) == 8 && turns_of_8(p) >= int64_t(4) * (kTcKeys / kTile) * kTcResident * sm_count();
+}
+
+// Its tensor map wants the codes at a multiple of 32 bytes and rows that
 // an int counts.
 bool make_codes_map(CUtensorMap *map, const Kv4AttnLaunch &p) {
   const int64_t rows = static_cast<int64_t>(p.cache.num_pages) * p.Hk * DSV4_PAGE_POSITIONS;
@@ -1238,7 +1278,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnLaunch &q, void *ws, cudaStream_t 
   P.a = q;
   const int R = tile_rows(q);
   CUtensorMap map;
-  const bool tc = q.D == 128 && R == 8 && make_codes_map(&map, q);
+  const bool tc = tensor_scores(q) && make_codes_map(&map, q);
   P.ctas = sm_count() * (tc ? kTcResident : resident(q));
   P.key_log2 = tc ? 7 : 6;
   P.group = q.Hq / q.Hk;

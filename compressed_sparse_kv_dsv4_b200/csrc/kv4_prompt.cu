@@ -308,7 +308,8 @@ __device__ void softmax_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const Pro
         h[k] = pack_half2(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
       *reinterpret_cast<uint4 *>(&S.q[t][i / 8][sw128_offset(r, i % 8)]) = make_uint4(h[0], h[1], h[2], h[3]);
     }
-    rs = p.softmax_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+    // (not below float32's normal numbers: a masked position is minus infinity times this)
+    rs = fmaxf(p.softmax_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23), 1.17549435e-38f);
   }
   fence_proxy_async_smem();
   __syncwarp();

@@ -552,6 +552,209 @@ def test_attention_leaves_the_rows_behind():
         check_attention(c, q, lens, [70, 0], out, lse, sample=8)
 
 
+# ---------------------------------------------------------------- few rows over tables with room for long contexts
+
+# Here a score also carries a rounding of q's elements 2^-14 below the row's largest, by at most 2^-22 of that. Of a
+# normal row one element in 4000 is that small (all are under 5): m of them move a score by m 2^-22 * 5 max |k| scale, while S
+# sums 128 products of means 0.8 each and max |k| is under 5: m 2^-22 * 25 / 80 S < m 2^-23 S, of the bound's 2^-16 S.
+
+ROOMY = [  # q heads, kv heads, new tokens, first positions
+    (8, 1, [1], [0]),
+    (8, 2, [1] * 8, [62, 63, 64, 126, 127, 128, 255, 256]),
+    (4, 4, [1, 1], [5, 700]),                    # one query head a key head
+    (6, 1, [1, 1, 1], [127, 129, 511]),          # rows that are not there
+    (4, 2, [4, 3, 0, 1], [60, 126, 900, 4]),     # draft tokens; a sequence that brings none
+    (16, 1, [1, 1], [999, 64]),                  # sixteen rows: two row tiles
+    (4, 1, [5, 6], [124, 250]),                  # row tiles that see fewer positions than the last
+    (32, 8, [1], [20000]),
+    (8, 1, [1, 1], [40000, 3]),
+    (16, 4, [1] * 150, [i * 13 % 700 for i in range(150)]),
+]
+
+
+def roomy(rng, lens, starts, Hk, fill=None):
+    return make_cache(rng, lens, starts, Hk, 128, fill=fill, extra_blocks=-(-1000 // (Hk * len(lens))))
+
+
+@pytest.mark.parametrize("case", ROOMY, ids=lambda c: f"{c[0]}over{c[1]}-{len(c[2])}-{max(c[3])}")
+@pytest.mark.parametrize("fill", [0xFF, 0xC8])
+def test_roomy_attention(case, fill):
+    require_gpu()
+    Hq, Hk, lens, starts = case
+    rng = np.random.default_rng(sum(starts) + Hq)
+    c = roomy(rng, lens, starts, Hk, fill)  # what lies behind the ends is NaN, or infinite in fp16
+    fill_cache(rng, c, lens, starts)
+    q, _ = rand_rows(rng, sum(lens), Hq, 128, torch.bfloat16, 2)
+    first = None
+    for max_new in (max(lens), 1):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = dsv4.kv4_attention(q, cu_of(lens), i32(starts), c, max_new=max_new, with_lse=True, d_status=st)
+        assert st.item() == 0
+        check_attention(c, q, lens, starts, out, lse, sample=24, ctx=f"max_new {max_new}")
+        if first is None:
+            first = (out, lse)
+            again = dsv4.kv4_attention(q, cu_of(lens), i32(starts), c, max_new=max_new, with_lse=True)
+            assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+def test_roomy_scales_and_rising_scores():
+    """Large scores whose maximum moves along the keys, in both directions; rows far from 1."""
+    require_gpu()
+    rng = np.random.default_rng(31)
+    lens, starts = [2, 1], [1500, 3000]
+    for order in (1, -1):
+        c = roomy(rng, lens, starts, 2)
+        tot = [n + s for n, s in zip(lens, starts)]
+        k, _ = rand_rows(rng, sum(tot), 2, 128, torch.bfloat16)
+        v, _ = rand_rows(rng, sum(tot), 2, 128, torch.bfloat16)
+        ramp = torch.cat([torch.linspace(0.01, 30, n, device="cuda") for n in tot])[:, None, None]
+        dsv4.kv4_append((k * (ramp if order > 0 else ramp.flip(0))).bfloat16(), v, cu_of(tot), i32([0, 0]), c, rope_dims=0)
+        q, _ = rand_rows(rng, 3, 4, 128, torch.bfloat16)
+        for mul, scale in ((1.0, 0.7), (2.0 ** 60, 2.0 ** -62), (2.0 ** -100, 2.0 ** 97)):
+            out, lse = dsv4.kv4_attention(q * mul, cu_of(lens), i32(starts), c, max_new=2, softmax_scale=scale, with_lse=True)
+            check_attention(c, q * mul, lens, starts, out, lse, scale=scale)
+    # scores that vanish, under a factor below float32's normal numbers: the mean of the values
+    out = dsv4.kv4_attention(q * 2.0 ** -100, cu_of(lens), i32(starts), c, max_new=2, softmax_scale=2.0 ** -60)
+    for s, at in ((0, 1), (1, 2)):
+        _, vv = cache_rows(c, s, tot[s])
+        mean = np.repeat(vv.mean(0), 2, 0)
+        assert np.all(np.abs(out[at].double().cpu().numpy() - mean) <= BF16 * np.abs(mean) + 2.0 ** -10 * np.abs(vv).mean(0).max())
+
+
+def test_roomy_elements_of_all_magnitudes():
+    """Rows of q whose elements lie up to 2^-30 apart: the bound's term for the small ones, by the largest."""
+    require_gpu()
+    rng = np.random.default_rng(32)
+    lens, starts = [1, 1], [700, 33]
+    c = roomy(rng, lens, starts, 1)
+    fill_cache(rng, c, lens, starts)
+    q, _ = rand_rows(rng, 2, 8, 128, torch.bfloat16)
+    q = (q * torch.exp2(-torch.from_numpy(rng.integers(0, 30, (2, 8, 128))).cuda().double())).bfloat16()
+    out, lse = dsv4.kv4_attention(q, cu_of(lens), i32(starts), c, max_new=1, softmax_scale=4.0, with_lse=True)
+    qv = q.double().cpu().numpy()
+    for s in range(2):
+        kk, vv = cache_rows(c, s, starts[s] + 1)
+        want, wl, mag, top = K.attention(qv[s:s + 1], kk, vv, starts[s], 4.0)
+        lost = 4.0 * 2.0 ** -22 * np.abs(qv[s]).max(-1) * np.abs(kk).sum(-1).max()
+        eps = 2 * 132 * U * top + lost + 2.0 ** -21 + 2 * U * 1.4427 * (top + np.abs(wl))
+        limit = (2.0 ** -11 + 2 * eps[..., None]) * mag + 2.0 ** -32 * np.abs(vv).sum(0) + BF16 * np.abs(want)
+        assert np.all(np.abs(out[s].double().cpu().numpy() - want[0]) <= limit[0])
+        assert np.all(np.abs(lse[s].double().cpu().numpy() - wl[0]) <= (eps + 4 * U * np.abs(wl) + 2.0 ** -21)[0])
+
+
+def test_roomy_nan_stays_with_the_rows_that_see_it():
+    require_gpu()
+    rng = np.random.default_rng(33)
+    for new, Hq in ((1, 16), (4, 4)):
+        lens, starts = [new], [600]
+        c = roomy(rng, lens, starts, 2)
+        fill_cache(rng, c, lens, starts)
+        q, _ = rand_rows(rng, new, Hq, 128, torch.bfloat16)
+        g = Hq // 2
+        run = lambda q=q: dsv4.kv4_attention(q, cu_of(lens), i32(starts), c, max_new=new, with_lse=True)
+        clean, lse0 = run()
+        for where in {600 + new // 2, 600 + new - 1, 5}:
+            page, row = c.block_table[0, where // PAGE].item(), where % PAGE
+            sees = torch.arange(new, device="cuda") + 600 >= where
+            for scales, head, blk, cols in ((c.v_scales, 1, 2, slice(64, 96)), (c.k_scales, 0, 1, slice(None))):
+                old = scales[page, head, row, blk].clone()
+                scales[page, head, row, blk] = 255
+                out, lse = run()
+                scales[page, head, row, blk] = old
+                want = torch.zeros_like(out, dtype=torch.bool)
+                want[:, head * g:(head + 1) * g, cols] = sees[:, None, None]
+                assert torch.equal(out.isnan(), want) and torch.equal(out[~want], clean[~want])
+                assert torch.equal(lse.isnan(), want[..., 0] if scales is c.k_scales else torch.zeros_like(lse, dtype=torch.bool))
+        for x in (float("nan"), float("inf")):
+            bad = q.clone()
+            bad[0, 1, 77] = x
+            out, lse = run(bad)
+            assert out[0, 1].isnan().all() and lse[0, 1].isnan()
+            out[0, 1], lse[0, 1] = clean[0, 1], lse0[0, 1]
+            assert torch.equal(out, clean) and torch.equal(lse, lse0)
+
+
+def test_roomy_bad_pages_and_rows_behind():
+    require_gpu()
+    rng = np.random.default_rng(34)
+    lens, starts = [1, 1], [600, 20]
+    c = roomy(rng, lens, starts, 1)
+    fill_cache(rng, c, lens, starts)
+    q, _ = rand_rows(rng, 5, 4, 128, torch.bfloat16)
+    out = torch.full((5, 4, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((5, 4), 3.0, device="cuda")
+    good = dsv4.kv4_attention(q, cu_of(lens), i32(starts), c, max_new=1, out=out, lse=lse)
+    assert torch.all(out[2:] == 3) and torch.all(lse[2:] == 3)
+    good = good.clone()
+    kk, vv = cache_rows(c, 0, 601)
+    keep = [j for j in range(601) if not 256 <= j < 512]
+    for spoil in (1 << 30, -1, c.k_codes.shape[0]):
+        old = c.block_table[0, 1].clone()
+        c.block_table[0, 1] = spoil
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        o, l = dsv4.kv4_attention(q[:2], cu_of(lens), i32(starts), c, max_new=1, with_lse=True, d_status=st)
+        c.block_table[0, 1] = old
+        assert st.item() == A.DEV_BAD_PAGE and torch.equal(o[1], good[1])
+        want, wl, mag, top = K.attention(q[:1].double().cpu().numpy(), kk[keep], vv[keep], len(keep) - 1, 128 ** -0.5)
+        eps = 2 * 132 * U * top + 2.0 ** -21 + 2 * U * 1.4427 * (top + np.abs(wl))
+        limit = (2.0 ** -11 + 2 * eps[..., None]) * mag + BF16 * np.abs(want)
+        assert np.all(np.abs(o[0].double().cpu().numpy() - want[0]) <= limit[0])
+    gone = dsv4.DeviceKv4Cache(c.k_codes, c.v_codes, c.k_scales, c.v_scales, torch.full_like(c.block_table, -1))
+    o, l = dsv4.kv4_attention(q[:2], cu_of(lens), i32(starts), gone, max_new=1, with_lse=True)
+    assert torch.all(o == 0) and torch.all(l == -np.inf)
+    for start in ([600, -1], [2 ** 31 - 1, 20]):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        dsv4.kv4_attention(q[:2], cu_of(lens), i32(start), c, max_new=1, with_lse=True, d_status=st)
+        assert st.item() & A.DEV_BAD_LENGTH
+
+
+def test_roomy_codes_at_any_sixteen_bytes():
+    """Codes that start 16 bytes off a multiple of 32 are read all the same."""
+    require_gpu()
+    rng = np.random.default_rng(35)
+    lens, starts = [1, 1], [300, 90]
+    c = roomy(rng, lens, starts, 1)
+    fill_cache(rng, c, lens, starts)
+    raw = torch.empty(c.k_codes.numel() + 64, dtype=torch.uint8, device="cuda")
+    at = (16 - raw.data_ptr()) % 32
+    moved = raw[at:at + c.k_codes.numel()].view(c.k_codes.shape)
+    moved.copy_(c.k_codes)
+    c2 = dsv4.DeviceKv4Cache(moved, c.v_codes, c.k_scales, c.v_scales, c.block_table)
+    q, _ = rand_rows(rng, 2, 8, 128, torch.bfloat16)
+    for x in (c, c2):
+        out, lse = dsv4.kv4_attention(q, cu_of(lens), i32(starts), x, max_new=1, with_lse=True)
+        check_attention(x, q, lens, starts, out, lse)
+
+
+def test_roomy_graphs():
+    """Captured beside other attention kernels that take tensor memory, replayed over a cache that has moved on."""
+    require_gpu()
+    rng = np.random.default_rng(36)
+    lens, starts = [1, 1], [250, 90]
+    c = roomy(rng, lens, [260, 100], 2)
+    fill_cache(rng, c, [0, 0], [260, 100])
+    q, _ = rand_rows(rng, 2, 8, 128, torch.bfloat16)
+    many, _ = rand_rows(rng, 300, 8, 128, torch.bfloat16)
+    start, cu, one = i32(starts), cu_of(lens), i32([0])
+    first = dsv4.DeviceKv4Cache(c.k_codes, c.v_codes, c.k_scales, c.v_scales, c.block_table[:1, :4].contiguous())
+
+    cu150 = cu_of([150])
+    dsv4.kv4_attention(q, cu, start, c, max_new=1)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a = dsv4.kv4_attention(q, cu, start, c, max_new=1, with_lse=True)
+        b = dsv4.kv4_attention(many[:150], cu150, one, first, max_new=150, with_lse=True)
+        d = dsv4.kv4_attention(q, cu, start, c, max_new=1, with_lse=True)
+    for s in (starts, [256, 91], [0, 0]):
+        start.copy_(i32(s))
+        g.replay()
+        torch.cuda.synchronize()
+        check_attention(c, q, lens, s, *a)
+        assert torch.equal(a[0], d[0]) and torch.equal(a[1], d[1])
+        check_attention(first, many[:150], [150], [0], *b, sample=8)
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("D,Hq,Hk", [(128, 8, 2), (64, 6, 3)])
