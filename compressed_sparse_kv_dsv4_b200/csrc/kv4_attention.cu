@@ -6,7 +6,7 @@
 // a unit of work is a row tile of R = 8 NT of them, of one key/value head of one sequence.
 //
 // Bound by memory when the rows are few: each cached value is 4.25 bits and is used once per
-// row tile. So all units' keys, in tiles of 64, form one line that is cut into equal slices,
+// row tile. So all units' keys, in tiles of 64 (or 128), form one line that is cut into equal slices,
 // one per CTA, whatever the sequences' lengths: every CTA reads the same number of bytes, and a
 // long sequence is split over many CTAs. A unit that one CTA has whole is written directly; the
 // parts of the others go through the workspace and kv4_combine_kernel joins them (a fixed
@@ -19,7 +19,8 @@
 // meet only there, and sixteen of them fit an SM at 128 registers. What bounds the kernel is their
 // instructions, some 1340 a tile of 16384 values at 128 channels (conversions, products with the scales,
 // 64 matrix products): 263 us for four sequences of 262144 positions (1.14 GB, 66% of the measured copy rate), 195 us
-// with the arithmetic left out.
+// with the arithmetic left out. (The form further down, whose scores are made on the tensor cores, takes long contexts
+// of up to eight rows at 128 channels: 240 us.)
 // The matrix products are mma.sync m16n8k16 (fp16 operands, fp32 sums) with
 // keys (S^T = K Q^T) and channels (O^T = V^T P^T) on the 16-row side and rows on the 8-column
 // side: a decode step has G rows, far fewer than a tcgen05 tile's 128, and the operand is made in
@@ -680,6 +681,11 @@ __global__ void __launch_bounds__(kThreadsA, StepShape<D, NT>::kResident)
 // memory, from where it is the B operand of mma.sync with the values as in the kernel above.
 // The reference of the weights is an integer (so that taking it off twice rounds alike), raised when a score exceeds
 // it by more than 2^8; weights are held times 2^7.
+// Measured: four sequences of 262144 positions 240 us (4.75 TB/s, 72% of the measured copy rate), 194 us with the
+// arithmetic left out, 195 us without the values' part of it, no less without the copies of the keys. What is left is
+// that part: 300 of a warp's 440 instructions for 32 keys, on three such warps a scheduler. Four CTAs an SM at
+// 96 registers (joins over the keys' stages to make room) took 256 us, one wait for all of a tile's scores in place of
+// two 249 us against 247 us, and values brought to registers before the weights were no faster.
 constexpr int kTcKeys = 128;
 constexpr int kTcThreads = 32 * (kWarps + 1);
 constexpr int kTcResident = 3;

@@ -569,6 +569,7 @@ ROOMY = [  # q heads, kv heads, new tokens, first positions
     (32, 8, [1], [20000]),
     (8, 1, [1, 1], [40000, 3]),
     (16, 4, [1] * 150, [i * 13 % 700 for i in range(150)]),
+    (2, 1, [0 if i % 7 == 3 else 1 for i in range(330)], [i * 37 % 290 for i in range(330)]),
 ]
 
 
