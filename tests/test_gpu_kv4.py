@@ -756,6 +756,83 @@ def test_roomy_graphs():
         check_attention(first, many[:150], [150], [0], *b, sample=8)
 
 
+def test_roomy_pool_of_more_than_32_bits():
+    """The last pages of a pool of 4.7 GB of keys and as much of values, under a wide table."""
+    require_gpu()
+    rng = np.random.default_rng(37)
+    pages = 36000
+    bt = np.full((2, 70), -1, dtype=np.int32)
+    bt[:, :2] = [[pages - 1, 3], [pages - 2, pages - 3]]
+    c = dsv4.DeviceKv4Cache.zeros(pages, 8, 128, dev(bt))
+    lens, starts = [1, 1], [300, 200]
+    fill_cache(rng, c, lens, starts)
+    q, _ = rand_rows(rng, 2, 16, 128, torch.bfloat16)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = dsv4.kv4_attention(q, cu_of(lens), i32(starts), c, max_new=1, with_lse=True, d_status=st)
+    assert st.item() == 0
+    check_attention(c, q, lens, starts, out, lse)
+
+
+def test_roomy_first_call_may_be_captured():
+    require_gpu()
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch, compressed_sparse_kv_dsv4_b200 as dsv4
+dsv4.load()
+def i32(v): return torch.tensor(v, dtype=torch.int32, device='cuda')
+c = dsv4.DeviceKv4Cache.zeros(8, 1, 128, i32([[1, 2] + [-1] * 998]))
+k = torch.randn(300, 1, 128, device='cuda').bfloat16()
+q = torch.randn(1, 4, 128, device='cuda').bfloat16()
+dsv4.kv4_append(k, k, i32([0, 300]), i32([0]), c, rope_dims=0)
+cu, start = i32([0, 1]), i32([299])
+ws = dsv4.kv4_attention_workspace(q, cu, c, max_new=1)
+out = torch.empty_like(q)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    dsv4.kv4_attention(q, cu, start, c, max_new=1, out=out, workspace=ws)
+g.replay()
+torch.cuda.synchronize()
+got = out.clone()
+dsv4.kv4_attention(q, cu, start, c, max_new=1, out=out, workspace=ws)
+torch.cuda.synchronize()
+assert torch.equal(got, out) and out.float().abs().max() > 0
+print('captured')
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_roomy_calls_beside_others():
+    """Steps on two streams and a prompt on a third at once, each with its own workspace: all want tensor memory."""
+    require_gpu()
+    rng = np.random.default_rng(38)
+    lens, starts = [1] * 4, [3000, 700, 90, 0]
+    c = roomy(rng, lens, starts, 4)
+    fill_cache(rng, c, lens, starts)
+    q, _ = rand_rows(rng, 4, 32, 128, torch.bfloat16)
+    many, _ = rand_rows(rng, 600, 32, 128, torch.bfloat16)
+    first = dsv4.DeviceKv4Cache(c.k_codes, c.v_codes, c.k_scales, c.v_scales, c.block_table[:1, :12].contiguous())
+    calls = [(q, cu_of(lens), i32(starts), c, 1), (q, cu_of(lens), i32(starts), c, 1), (many, cu_of([600]), i32([2000]), first, 600)]
+    alone = [dsv4.kv4_attention(a, cu, st, x, max_new=m) for a, cu, st, x, m in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    spaces = [dsv4.kv4_attention_workspace(a, cu, x, max_new=m) for a, cu, st, x, m in calls]
+    outs = [torch.zeros_like(o) for o in alone]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for (a, cu, st, x, m), s, ws, o in zip(calls, streams, spaces, outs):
+            with torch.cuda.stream(s):
+                dsv4.kv4_attention(a, cu, st, x, max_new=m, out=o, workspace=ws)
+    torch.cuda.synchronize()
+    for o, want in zip(outs, alone):
+        assert torch.equal(o, want)
+    check_attention(c, q, lens, starts, *dsv4.kv4_attention(*calls[0][:4], max_new=1, with_lse=True))
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("D,Hq,Hk", [(128, 8, 2), (64, 6, 3)])
