@@ -700,14 +700,18 @@ struct alignas(1024) TcStepSmem {
   struct alignas(128) Values {
     uint8_t c[kTcKeys * 64], ks[kTcKeys * 4], vs[kTcKeys * 4];
   } v[2];
-  uint4 pw[kWarps][32];            // weights of a warp's keys, fp16
-  float o[kWarps][8][128 + 4];
+  union {
+    uint4 pw[kWarps][32];          // weights of a warp's keys, fp16
+    int64_t prefix[kTcThreads + 1];  // before the first product
+  };
+  alignas(16) uint16_t sv[kWarps][4][4][8];  // scales of a warp's values, fp16, per block in the order of the products
+  alignas(16) float o[kWarps][8][128 + 4];
   float2 ml[kWarps][8];
   float keep[kWarps][8];
   alignas(16) float rs[8];         // log2 score per product
   alignas(16) int lim[8];
   int64_t index[8];
-  int64_t prefix[kTcThreads + 1], warp_sums[kTcThreads / 32];
+  int64_t warp_sums[kTcThreads / 32];
   uint64_t k_full[2], v_full[2], v_free[2], s_full[2], s_free[2], q_full;
   int bad[2];
   int nan_at[128 / kKv4Block];
@@ -830,6 +834,9 @@ __device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Wa
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
   const uint32_t pw_at = smem_u32(&S.pw[warp][8 * (lane >> 3) + key_of(lane & 7)]);
+  // where this lane's key's value scales go: halves [block][t4][16-key group][+ 8][first or second of the pair]
+  const int lane_row = (0x1320 >> (4 * (lane & 3))) & 3;  // the inverse of key_of
+  uint16_t *const sv_to = &S.sv[warp][0][0][0] + ((lane & 4) / 2 + (lane_row >> 1)) * 8 + (lane >> 4) * 4 + (lane >> 3 & 1) * 2 + (lane_row & 1);
   uint32_t n = 0;  // tiles of the CTA
   bool dead = false;
   auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -903,6 +910,22 @@ __device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Wa
       const int key0 = (w.tile + i) * kTcKeys + 32 * warp;  // the warp's first key
       const bool edge = key0 + 32 > least;
       const uint32_t kb = *reinterpret_cast<const uint32_t *>(T.ks + 4 * (32 * warp + lane));
+      uint32_t vb = *reinterpret_cast<const uint32_t *>(T.vs + 4 * (32 * warp + lane));
+      if ((edge || bad) && (bad || key0 + lane >= limit)) vb = 0;  // not a position of the unit
+      if (vb & vb << 1 & 0x80808080u) {  // no scale but NaN's byte has its two upper bits
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if ((vb >> (8 * b) & 255u) == 255u) {
+            atomicMin(&S.nan_at[b], key0 + lane);
+            vb &= ~(255u << (8 * b));
+          }
+      }
+      {
+        auto power = [&](int b) { return __uint_as_float((vb >> (8 * b) & 255u) << 23); };
+        const uint32_t h01 = pack_half2(power(0), power(1)), h23 = pack_half2(power(2), power(3));
+        sv_to[0] = static_cast<uint16_t>(h01), sv_to[32] = static_cast<uint16_t>(h01 >> 16);
+        sv_to[64] = static_cast<uint16_t>(h23), sv_to[96] = static_cast<uint16_t>(h23 >> 16);
+      }
       const uint32_t s_at = tmem + 64 * slot + (static_cast<uint32_t>(32 * warp) << 16);
       uint64_t s[R / 2];
 #pragma unroll
@@ -986,33 +1009,18 @@ __device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Wa
       __syncwarp();
       uint32_t pb[4];
       ldmatrix4_trans(pb, pw_at);
+      const uint4 sv = *reinterpret_cast<const uint4 *>(S.sv[warp][g >> 1][t4]);
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
         const int kA = 16 * mt + key_of(2 * t4), kB = 16 * mt + key_of(2 * t4 + 1);  // of the warp's 32
         uint32_t c4[4][2];
-        float sf[4];
-        const int blk = g >> 1;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int key = 32 * warp + ((q & 1) ? kB : kA) + (q >> 1) * 8;
           const uint2 v = *reinterpret_cast<const uint2 *>(T.c + key * 64 + g * 8);
           c4[q][0] = v.x, c4[q][1] = v.y;
-          sf[q] = __uint_as_float(static_cast<uint32_t>(T.vs[key * 4 + blk]) << 23);
         }
-        if (edge || bad) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)  // not a position of the unit
-            if (bad || key0 + ((q & 1) ? kB : kA) + (q >> 1) * 8 >= limit) sf[q] = 0.f;
-        }
-        if ((sf[0] + sf[1]) + (sf[2] + sf[3]) == INFINITY) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (sf[q] == INFINITY) {
-              atomicMin(&S.nan_at[blk], key0 + ((q & 1) ? kB : kA) + (q >> 1) * 8);
-              sf[q] = 0.f;
-            }
-        }
-        const uint32_t sAB = pack_half2(sf[0], sf[1]), sCD = pack_half2(sf[2], sf[3]);
+        const uint32_t sAB = mt == 0 ? sv.x : sv.z, sCD = mt == 0 ? sv.y : sv.w;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t lo[2][4], hi[2][4];  // as in the kernel above
