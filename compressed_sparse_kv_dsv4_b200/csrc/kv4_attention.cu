@@ -935,7 +935,7 @@ __device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Wa
         tmem_ld_wait();
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const float f = scale_value(kb >> (8 * (2 * h + b)) & 255u);
+          const float f = __uint_as_float((kb >> (8 * (2 * h + b)) & 255u) << 23);
           const uint64_t f2 = pack_f32x2(f, f), part = pack_f32x2(0.03125f, 0.03125f);
 #pragma unroll
           for (int k = 0; k < R / 2; ++k) {
@@ -949,6 +949,14 @@ __device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Wa
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.s_free[slot]);
+      if (kb & kb << 1 & 0x80808080u) {  // a NaN block makes the key's scores NaN
+        bool nan = false;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) nan |= (kb >> (8 * b) & 255u) == 255u;
+#pragma unroll
+        for (int k = 0; k < R / 2; ++k)
+          if (nan) s[k] = pack_f32x2(__uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u));
+      }
       if (edge || bad) {
 #pragma unroll
         for (int k = 0; k < R / 2; ++k) {
@@ -961,21 +969,19 @@ __device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Wa
           s[k] = pack_f32x2(a, b);
         }
       }
-      uint64_t rs[R / 2];
-#pragma unroll
-      for (int k = 0; k < R / 2; ++k) rs[k] = *reinterpret_cast<const uint64_t *>(&S.rs[2 * k]);
+      auto rs = [&](int k) { return *reinterpret_cast<const uint64_t *>(&S.rs[2 * k]); };
       float y[R];
       float most = -INFINITY;
 #pragma unroll
       for (int k = 0; k < R / 2; ++k) {
-        unpack_f32x2(fma_f32x2(s[k], rs[k], off[k]), y[2 * k], y[2 * k + 1]);
+        unpack_f32x2(fma_f32x2(s[k], rs(k), off[k]), y[2 * k], y[2 * k + 1]);
         most = fmaxf(most, fmaxf(y[2 * k], y[2 * k + 1]));
       }
       if (__any_sync(0xFFFFFFFFu, most > kTcOff + kTcRaise)) {
 #pragma unroll
         for (int k = 0; k < R / 2; ++k) {
           float x[2], f[2], sums[2];
-          unpack_f32x2(mul_f32x2(s[k], rs[k]), x[0], x[1]);
+          unpack_f32x2(mul_f32x2(s[k], rs(k)), x[0], x[1]);
           unpack_f32x2(off[k], f[0], f[1]);
           unpack_f32x2(l[k], sums[0], sums[1]);
 #pragma unroll
@@ -990,7 +996,7 @@ __device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Wa
           }
           off[k] = pack_f32x2(f[0], f[1]);
           l[k] = pack_f32x2(sums[0], sums[1]);
-          unpack_f32x2(fma_f32x2(s[k], rs[k], off[k]), y[2 * k], y[2 * k + 1]);
+          unpack_f32x2(fma_f32x2(s[k], rs(k), off[k]), y[2 * k], y[2 * k + 1]);
         }
         __syncwarp();
         const float2 keep = *reinterpret_cast<const float2 *>(&S.keep[warp][2 * t4]);
