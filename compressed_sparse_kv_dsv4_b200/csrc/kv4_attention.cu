@@ -20,7 +20,7 @@
 // instructions, some 1340 a tile of 16384 values at 128 channels (conversions, products with the scales,
 // 64 matrix products): 263 us for four sequences of 262144 positions (1.14 GB, 66% of the measured copy rate), 195 us
 // with the arithmetic left out. (The form further down, whose scores are made on the tensor cores, takes long contexts
-// of up to eight rows at 128 channels: 240 us.)
+// of up to eight rows at 128 channels: 225 us.)
 // The matrix products are mma.sync m16n8k16 (fp16 operands, fp32 sums) with
 // keys (S^T = K Q^T) and channels (O^T = V^T P^T) on the 16-row side and rows on the 8-column
 // side: a decode step has G rows, far fewer than a tcgen05 tile's 128, and the operand is made in
@@ -681,11 +681,12 @@ __global__ void __launch_bounds__(kThreadsA, StepShape<D, NT>::kResident)
 // memory, from where it is the B operand of mma.sync with the values as in the kernel above.
 // The reference of the weights is an integer (so that taking it off twice rounds alike), raised when a score exceeds
 // it by more than 2^8; weights are held times 2^7.
-// Measured: four sequences of 262144 positions 240 us (4.75 TB/s, 72% of the measured copy rate), 194 us with the
+// Measured: four sequences of 262144 positions 225 us (5.07 TB/s, 77% of the measured copy rate); 194 us with the
 // arithmetic left out, 195 us without the values' part of it, no less without the copies of the keys. What is left is
-// that part: 300 of a warp's 440 instructions for 32 keys, on three such warps a scheduler. Four CTAs an SM at
-// 96 registers (joins over the keys' stages to make room) took 256 us, one wait for all of a tile's scores in place of
-// two 249 us against 247 us, and values brought to registers before the weights were no faster.
+// that part, on three such warps a scheduler: its conversions some 33 us, the products with the scales 7 us, mma.sync
+// nothing. The values' scales are converted once a warp and shared (each lane for itself: 240 us). Four CTAs an SM at
+// 96 registers took 256 us against 247 us then, one wait for all of a tile's scores 249 us, and values brought to
+// registers before the weights were no faster.
 constexpr int kTcKeys = 128;
 constexpr int kTcThreads = 32 * (kWarps + 1);
 constexpr int kTcResident = 3;
@@ -1120,10 +1121,11 @@ __global__ void __launch_bounds__(kTcThreads, kTcResident)
 // Joins the parts of a unit that several slices share. All slices but the first of a unit start inside it: their
 // CTAs here share its sums out, and the lanes of a CTA the parts of a sum, in an order that the number of slices fixes.
 // (With one CTA joining a unit, a call for one sequence of 32000 positions, 74 slices to each of 8 units, took 35.4 us;
-// so it takes 20.7 us. One of 131000: 59 us and 46 us.)
+// so it takes 20.7 us. One of 131000: 59 us and 46 us. With eight loads at a time and 80 registers, not 64, 8 sequences
+// of 32000 positions took 90 us in place of 81 us.)
 constexpr int kCombineThreads = 128;
 template <int D>
-__global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const __grid_constant__ AttnParams P, int R) {
+__global__ void __launch_bounds__(kCombineThreads, 8) kv4_combine_kernel(const __grid_constant__ AttnParams P, int R) {
   __shared__ int64_t prefix[kCombineThreads + 1], warp_sums[kCombineThreads / 32];
   const Kv4AttnLaunch &p = P.a;
   // (this grid starts once every CTA of the step kernel is past its own wait, so the lengths, which the
@@ -1154,7 +1156,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const __gr
   pdl_wait();
   pdl_launch_dependents();
   if (!mine) return;
-  constexpr int V4 = D / 4, kAtOnce = 8;
+  constexpr int V4 = D / 4, kAtOnce = 4;
   const int parts = last - first + 1, rank = c - first - 1;
   const int e0 = R * V4 * rank / (parts - 1), e1 = R * V4 * (rank + 1) / (parts - 1);
   int lanes = 1;  // of a sum
@@ -1166,7 +1168,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const __gr
     const bool there = e < e1 && w.row_limit(r) > 0;
     float mx = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = first + mine_at; there && k0 <= last; k0 += kAtOnce * lanes) {  // eight parts' loads at a time
+    for (int k0 = first + mine_at; there && k0 <= last; k0 += kAtOnce * lanes) {  // four parts' loads at a time
       float2 ml[kAtOnce];
       float4 v[kAtOnce];
 #pragma unroll
@@ -1254,9 +1256,9 @@ cudaError_t launch_step(AttnParams &P, cudaStream_t st) {
 
 // The form with scores on the tensor cores takes calls of at least four of its tiles for each of its CTAs, going by the
 // longest context that the table holds; with fewer its start and its longer turns show. At 8 key heads of 8 query
-// heads each, the kernel above and this one: 8 sequences of 2000 positions (1024 tiles) 16.6 us and 20.6 us, one of
-// 32000 (2000) 22.0 us and 24.7 us; 64 of 500 (2048) 35.1 us and 27.8 us, 8 of 8000 (4096) 37.7 us and 30.4 us, 8 of
-// 32000 89.3 us and 74.5 us.
+// heads each, the kernel above and this one: 8 sequences of 2000 positions (1024 tiles) 15.7 us and 20.0 us, one of
+// 32000 (2000) 21.4 us and 24.7 us; 64 of 500 (2048) 33.9 us and 26.8 us, 8 of 8000 (4096) 31.8 us and 28.8 us, 8 of
+// 32000 81.4 us and 70.4 us.
 bool tensor_scores(const Kv4AttnLaunch &p) {
   return p.D == 128 && tile_rows(p) == 8 && turns_of_8(p) >= int64_t(4) * (kTcKeys / kTile) * kTcResident * sm_count();
 }
