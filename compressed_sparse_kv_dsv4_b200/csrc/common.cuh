@@ -102,7 +102,9 @@ __device__ __forceinline__ void rope_cos_sin(int64_t pos, int pair, double theta
 // prerequisite grid has completed and its memory is visible; before it a kernel may only
 // touch data no predecessor writes or reads. Each kernel calls pdl_launch_dependents()
 // after its own pdl_wait(), so a kernel's early part only ever overlaps its immediate
-// predecessor. Launched without the attribute, both are no-ops.
+// predecessor. Only a kernel that another one of the same call follows releases it: first kernels of
+// a call may read the caller's inputs, and write the workspace, before they wait. Launched without
+// the attribute, both are no-ops.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kThreadsA, StepShape<D, NT>::kResident)
     fence_mbar_init();
   }
   pdl_wait();
-  pdl_launch_dependents();
+  pdl_launch_dependents();  // (the join follows in this call)
   const Line line{&p, P.group, R, 31 - __clz(R), P.key_log2};
   const int chunk = (p.B + kThreadsA - 1) / kThreadsA;
   const int64_t all = line_prefix(line, kThreadsA, chunk, S.prefix, S.warp_sums);
@@ -1091,7 +1091,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcResident)
     prefetch_tensormap(&map);
   }
   pdl_wait();
-  // (between the two: a kernel that this one waits for, or that waits for this one, may want all of TMEM)
+  // (not before the wait: a kernel that this one waits for may want all of TMEM)
   if (warp == kWarps) {
     tmem_alloc(&S.tmem_base, kTcCols);
     tmem_relinquish();
@@ -1101,7 +1101,7 @@ __global__ void __launch_bounds__(kTcThreads, kTcResident)
   const int chunk = (p.B + kTcThreads - 1) / kTcThreads;
   const int64_t all = line_prefix(line, kTcThreads, chunk, S.prefix, S.warp_sums);
   tc_fence_after();
-  pdl_launch_dependents();
+  pdl_launch_dependents();  // (the join follows in this call)
   const uint32_t tmem = __reduce_max_sync(0xFFFFFFFFu, S.tmem_base);
   const int ctas = slices(all, P.ctas, P.key_log2);
   if (static_cast<int>(blockIdx.x) < ctas) {
@@ -1153,8 +1153,7 @@ __global__ void __launch_bounds__(kCombineThreads, 8) kv4_combine_kernel(const _
       last = slice_of(from - w.tile + w.tiles - 1);
     }
   }
-  pdl_wait();
-  pdl_launch_dependents();
+  pdl_wait();  // (the last kernel of its call: it does not release the next call's kernels early)
   if (!mine) return;
   constexpr int V4 = D / 4, kAtOnce = 4;
   const int parts = last - first + 1, rank = c - first - 1;
@@ -1250,7 +1249,7 @@ template <int D, int NT>
 cudaError_t launch_step(AttnParams &P, cudaStream_t st) {
   const size_t smem = sizeof(AttnSmem<D, NT>) + 128;
   const cudaError_t e = launch_large<kv4_step_kernel<D, NT>>(dim3(P.ctas), dim3(kThreadsA), smem, st, P);
-  if (e != cudaSuccess || P.ctas == 1) return e;
+  if (e != cudaSuccess) return e;
   return launch_pdl(kv4_combine_kernel<D>, dim3(P.ctas - 1), dim3(kCombineThreads), 0, st, 1, P, 8 * NT);
 }
 
@@ -1281,7 +1280,7 @@ bool make_codes_map(CUtensorMap *map, const Kv4AttnLaunch &p) {
 cudaError_t launch_tc_step(AttnParams &P, const CUtensorMap &map, cudaStream_t st) {
   const cudaError_t e =
       launch_large<kv4_step_tc_kernel>(dim3(P.ctas), dim3(kTcThreads), sizeof(TcStepSmem) + 1024, st, P, map);
-  if (e != cudaSuccess || P.ctas == 1) return e;
+  if (e != cudaSuccess) return e;
   return launch_pdl(kv4_combine_kernel<128>, dim3(P.ctas - 1), dim3(kCombineThreads), 0, st, 1, P, 8);
 }
 

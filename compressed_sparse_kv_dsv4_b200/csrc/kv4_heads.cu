@@ -211,8 +211,7 @@ __global__ void __launch_bounds__(kHThreads, 3) kv4_heads_kernel(const __grid_co
   const bool cached = p.cache.k_codes != nullptr;
   const int pairs = p.rope_dims / 2, rope_at = D - p.rope_dims;
   const bool aligned = rope_at % 8 == 0;  // a lane's pairs are all turned or none, and start at a multiple of four
-  pdl_wait();
-  pdl_launch_dependents();
+  pdl_wait();  // (the only kernel of its call: it releases nothing early, the next call may read these rows at its start)
   for (int i = tid; i < 2 * D; i += kHThreads) {
     const float *src = i < D ? p.gamma_q : p.gamma_k;
     const int d = i % D;

@@ -448,6 +448,8 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
   constexpr uint32_t kCols = 512;
   // Blocks of later rows (more keys) come first; the sequences and heads of one block of rows are neighbours.
   const int shared_at = static_cast<int>(blockIdx.x) - P.whole;  // this CTA among those that share
+  // whether a join follows in this call (the last kernel of a call does not release the next call's early)
+  const bool joined = static_cast<unsigned>(P.whole) < gridDim.x;
   const int splits = shared_at < 0 ? 1 : P.splits, split = shared_at < 0 ? 0 : shared_at % splits;
   const int unit = shared_at < 0 ? static_cast<int>(blockIdx.x) : P.whole + shared_at / splits;
   const int heads = p.B * p.Hk, first_rb = P.row_blocks - 1 - unit / heads, s = unit % heads / p.Hk, kvh = unit % heads % p.Hk;
@@ -475,7 +477,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
   u.row0 = static_cast<int64_t>(first_rb) * 2 * kRows;
   const int tiles = u.row0 < u.rows ? max(u.tiles(0), u.tiles(1)) : 0;
   if (split * share_of(tiles, splits) >= tiles) {  // (no such rows, or nothing left for this split)
-    pdl_launch_dependents();
+    if (joined) pdl_launch_dependents();
     return;
   }
   if (warp == 12) {
@@ -485,9 +487,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // (not before the TMEM is held: a following kernel's CTA that took it while waiting for this grid
-  // would wait for ever)
-  pdl_launch_dependents();
+  if (joined) pdl_launch_dependents();
   const uint32_t tmem = __reduce_max_sync(0xFFFFFFFFu, S.tmem_base);
 
   // Every role walks over the CTA's units (more than one only where a sequence brings more new
@@ -575,8 +575,7 @@ __global__ void __launch_bounds__(kRows) kv4_prompt_combine_kernel(const __grid_
     const int Tt = u.tiles(t), share = share_of(max(u.tiles(0), u.tiles(1)), P.splits);
     parts = (Tt + share - 1) / share;
   }
-  pdl_wait();
-  pdl_launch_dependents();
+  pdl_wait();  // (the last kernel of its call: it does not release the next call's kernels early)
   if (row >= u.rows) return;
   const int64_t index = (u.q.tok0 + row / u.G) * p.Hq + u.kvh * u.G + row % u.G;
   const int64_t slot0 = static_cast<int64_t>(shared_at) * P.splits * 2 + t;
