@@ -8,9 +8,11 @@ import pytest
 import torch
 
 import compressed_sparse_kv_dsv4_b200 as dsv4
+import oracle.kv4_oracle as K
+import perf.operators as operators
 import synthetic as W
 from tests.parity import require_gpu
-from tests.test_gpu_kv4 import cu_of, fill_cache, i32, make_cache, rand_rows
+from tests.test_gpu_kv4 import (BF16, cu_of, dev, fill_cache, i32, make_cache, pair_bound, positions, rand_rows)
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +75,41 @@ def test_a_workspace_passes_to_the_next_call(new, D):
         got = dsv4.sparse_mqa_decode(dq, pos, dl.cache, dl.ring, workspace=ws, **args)
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(lse, lse0) and torch.equal(got, step)
+
+
+# ---------------------------------------------------------------- the append's queries
+
+@pytest.mark.parametrize("din", ["f32", "bf16"])
+@pytest.mark.parametrize("dout", ["f32", "bf16"])
+@pytest.mark.parametrize("D,Hq,Hk,rope,extra", [(64, 7, 1, 64, 0), (128, 12, 4, 44, 4)])
+def test_append_queries_in_both_types(D, Hq, Hk, rope, extra, din, dout):
+    require_gpu()
+    rng = np.random.default_rng(D + Hq)
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}
+    lens, starts = [33, 0, 5], [250, 9, 100003]
+    c = make_cache(rng, lens, starts, Hk, D)
+    T = sum(lens)
+    q, qv = rand_rows(rng, T, Hq, D, dt[din], extra)
+    k, _ = rand_rows(rng, T, Hk, D, dt[din], extra)
+    g = 1 + 0.3 * rng.standard_normal(D).astype(np.float32)
+    for gamma in (g, None):
+        out = torch.full((T + 3, Hq, D), 7.0, dtype=dt[dout], device="cuda")
+        got, ks, _ = dsv4.kv4_append(k, k, cu_of(lens), i32(starts), c, q=q, gamma_q=None if gamma is None else dev(g),
+                                     q_out=out[:T], rope_dims=rope, with_stored=True)
+        assert got.data_ptr() == out.data_ptr() and torch.all(out[T:] == 7) and ks.dtype == torch.bfloat16
+        want = K.norm_rotate(qv, gamma, 1e-6, positions(lens, starts), rope, 10000.0)
+        limit = pair_bound(want, rope) + (BF16 * np.abs(want) if dout == "bf16" else 0) + 1e-30
+        assert np.all(np.abs(got.double().cpu().numpy() - want) <= limit)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_measured_append_returns_what_its_plain_form_does(dtype, monkeypatch):
+    """perf/operators.py counts the queries' bytes in their own type: its calls ask for that type."""
+    require_gpu()
+    case = dict(op="append", batch=3, new=9, ctx=300, ragged=True, heads=4, kv_heads=2, dim=64, rope=32, dtype=dtype)
+    kinds = []
+    for own in (False, True):
+        monkeypatch.setattr(operators, "own", own)
+        got = operators.run(operators.prepare(case, 1))
+        kinds.append({n: (t.dtype, tuple(t.shape)) for n, t in got.items()})
+    assert kinds[0] == kinds[1]
