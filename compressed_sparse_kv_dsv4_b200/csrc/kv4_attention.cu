@@ -285,13 +285,14 @@ __device__ __forceinline__ void join_part(const AttnParams &P, Smem &S, const Wa
       acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
       acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
     }
+    if (mx == -INFINITY && sum == 0.f && row_sees(p, w.s, w.tile, stop, w.ln.key_log2, rl)) mx = kLeast;
     if (S.nan_at[d / kKv4Block] < rl) acc.x = acc.y = acc.z = acc.w = __uint_as_float(0x7FC00000u);
     if (whole) {
       const int64_t row = S.index[r];
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const float inv = row_inverse(mx, sum);
       const uint2 b = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
       *reinterpret_cast<uint2 *>(p.out + row * D + d) = b;
-      if (d == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (mx - kPOff + log2f(sum)) * 0.6931471805599453f;
+      if (d == 0 && p.lse) p.lse[row] = row_lse(mx, sum, kPOff);
     } else {
       *reinterpret_cast<float4 *>(P.part_o + (static_cast<int64_t>(part) * R + r) * D + d) = acc;
       if (d == 0) P.part_ml[part * R + r] = make_float2(mx, sum);
@@ -693,7 +694,7 @@ constexpr int kTcResident = 3;
 constexpr int kTcCols = 128;       // TMEM columns: two tiles of 4 blocks x 16
 constexpr float kTcOff = 7.f;      // weights are held times 2^7
 constexpr float kTcRaise = 8.f;
-constexpr float kTcNone = 3e38f;   // off of a row without a reference yet
+constexpr float kTcNone = -kLeast;  // off of a row without a reference yet
 
 struct alignas(1024) TcStepSmem {
   uint8_t k[2][kTcKeys * 128];     // codes, spread: 16 of them in each 16 bytes
@@ -859,7 +860,8 @@ __device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Wa
       for (int k = 0; k < 4; ++k) am = max(am, max((x[k] << 16) & 0x7FFF0000u, x[k] & 0x7FFF0000u));
 #pragma unroll
       for (int o2 = 1; o2 < 16; o2 <<= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, o2));
-      // 2^sh brings the largest element to [2^7, 2^8); a row with an infinity or NaN has no finite score
+      // 2^sh brings the largest element to [2^7, 2^8). A row with an infinity or NaN has no finite score: it goes in as
+      // e4m3's NaN, which makes NaN of the scores of the positions that the row sees (masked ones are set afterwards).
       const int ex = static_cast<int>(am >> 23) - 127;
       const int sh = (am == 0 || ex >= 128) ? 0 : min(max(7 - ex, -120), 120);
       const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
@@ -871,6 +873,7 @@ __device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Wa
         hi[k] = e4m3_pair(a, b, ha, hb);
         float la, lb;
         lo[k] = e4m3_pair((a - ha) * 32.f, (b - hb) * 32.f, la, lb);
+        if (ex >= 128) hi[k] = lo[k] = 0x7F7Fu;
       }
       const uint32_t at = sw128_offset(r, c >> 1) + 8 * (c & 1);
       *reinterpret_cast<uint2 *>(S.q + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
@@ -878,9 +881,8 @@ __device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Wa
       if (c == 0) {
         S.lim[r] = there ? min(w.q.n, w.q.start + static_cast<int>(i) + 1) : 0;
         S.index[r] = tok * p.Hq + head;
-        S.rs[r] = ex >= 128 ? __uint_as_float(0x7FC00000u)
-                            : fmaxf(p.softmax_scale * 1.4426950408889634f *
-                                        __uint_as_float(static_cast<uint32_t>(127 - sh) << 23), 1.17549435e-38f);
+        S.rs[r] = fmaxf(p.softmax_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23),
+                        1.17549435e-38f);
       }
       if (tid < D / kKv4Block) S.nan_at[tid] = 0x7FFFFFFF;
     }
@@ -1203,10 +1205,10 @@ __global__ void __launch_bounds__(kCombineThreads, 8) kv4_combine_kernel(const _
     }
     if (!there || mine_at != 0) continue;
     const int64_t row = w.row_index(r);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = row_inverse(mx, sum);
     *reinterpret_cast<uint2 *>(p.out + row * D + d) =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (d == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (mx - kPOff + log2f(sum)) * 0.6931471805599453f;
+    if (d == 0 && p.lse) p.lse[row] = row_lse(mx, sum, kPOff);
   }
 }
 

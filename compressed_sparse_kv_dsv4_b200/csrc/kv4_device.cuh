@@ -89,6 +89,26 @@ __device__ __forceinline__ bool seq_info(const Kv4AttnLaunch &p, int s, Seq *q, 
   return true;
 }
 
+// How a row's sums end. Its maximum (or reference) m is -infinity where the row saw no position, and
+// kLeast where it saw some and all their scores are -infinity (scores beyond float32, an infinite query): no position
+// gives zero and lse -infinity, the other NaN, as 0 / 0 does, so that neither passes for the other.
+constexpr float kLeast = -3.402823466e38f;
+__device__ __forceinline__ float row_inverse(float m, float sum) {
+  return sum != 0.f ? 1.f / sum : (m == -INFINITY ? 0.f : __uint_as_float(0x7FC00000u));
+}
+__device__ __forceinline__ float row_lse(float m, float sum, float off) {  // weights are held times 2^off
+  return sum != 0.f ? (m - off + log2f(sum)) * 0.6931471805599453f : (m == -INFINITY ? m : __uint_as_float(0x7FC00000u));
+}
+// Whether a row that sees positions below lim sees any of tiles first .. last - 1, of 2^keys_log2 keys (a tile lies on one
+// page). For rows without a finite score only: the table is looked up again.
+__device__ __forceinline__ bool row_sees(const Kv4AttnLaunch &p, int s, int first, int last, int keys_log2, int lim) {
+  for (int i = first; i < last && i << keys_log2 < lim; ++i) {
+    const int page = p.cache.block_table[static_cast<int64_t>(s) * p.cache.max_blocks + ((i << keys_log2) / DSV4_PAGE_POSITIONS)];
+    if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.cache.num_pages)) return true;
+  }
+  return false;
+}
+
 // a byte of two e2m1 codes -> fp16 pair; four bytes at once
 __device__ __forceinline__ void e2m1x8_to_half2(uint32_t w, uint32_t (&h)[4]) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"

@@ -27,7 +27,8 @@ namespace dsv4 {
 namespace {
 
 constexpr int kRows = 128;             // rows of a row tile
-constexpr int kKeys = 128;             // keys of a stage
+constexpr int kKeysLog2 = 7;
+constexpr int kKeys = 1 << kKeysLog2;  // keys of a stage
 constexpr int kPThreads = 512;         // 4 warpgroups
 constexpr float kRaise = 8.f;          // log2 that a maximum may exceed the reference by
 constexpr float kPOffP = 7.f;          // weights are held times 2^7
@@ -275,8 +276,8 @@ __device__ __forceinline__ void mma_role(PromptSmem<D> &S, uint32_t tmem, int T0
 }
 
 template <int D>
-__device__ void softmax_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const PromptUnit &u, uint32_t tmem, int t, int T,
-                             int kv, int &done, int &units, bool &dead, float4 *part_o, float2 *part_ml) {
+__device__ void softmax_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const PromptUnit &u, int seq, uint32_t tmem, int t,
+                             int T, int kv, int &done, int &units, bool &dead, float4 *part_o, float2 *part_ml) {
   const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
   const uint32_t lanes = static_cast<uint32_t>(threadIdx.x & 96) << 16;
   const uint32_t s_at = tmem + 128u * t + lanes, o_at = tmem + 256u + static_cast<uint32_t>(D * t) + lanes;
@@ -402,7 +403,8 @@ __device__ void softmax_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const Pro
       float l0, l1;
       unpack_f32x2(add_f32x2(la, lb), l0, l1);
       const float l = l0 + l1;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      if (R == -INFINITY && row_sees(p, seq, u.j0, u.j0 + T, kKeysLog2, lim)) R = kLeast;
+      const float inv = row_inverse(R, l);
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -430,7 +432,7 @@ __device__ void softmax_role(const Kv4AttnLaunch &p, PromptSmem<D> &S, const Pro
       }
       tc_fence_before();
       if (part_o) part_ml[r] = make_float2(R, l);
-      else if (lim > 0 && p.lse) p.lse[index] = l == 0.f ? -INFINITY : (R - kPOffP + log2f(l)) * 0.6931471805599453f;
+      else if (lim > 0 && p.lse) p.lse[index] = row_lse(R, l, kPOffP);
     } else {
       dead = true;
     }
@@ -524,7 +526,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const __grid_c
     units_loop([&](int T0, int T1) {
       const int t = warp / 4;
       const int64_t slot = part ? (static_cast<int64_t>(unit - P.whole) * splits + split) * 2 + t : 0;
-      softmax_role<D>(p, S, u, tmem, t, t == 0 ? T0 : T1, kv, done, n_units, dead,
+      softmax_role<D>(p, S, u, s, tmem, t, t == 0 ? T0 : T1, kv, done, n_units, dead,
                       part ? P.part_o + slot * (D / 4 * kRows) : nullptr, part ? P.part_ml + slot * kRows : nullptr);
     });
   } else if (warp < 12) {
@@ -597,13 +599,13 @@ __global__ void __launch_bounds__(kRows) kv4_prompt_combine_kernel(const __grid_
       acc[4 * i + 2] = fmaf(v.z, f, acc[4 * i + 2]), acc[4 * i + 3] = fmaf(v.w, f, acc[4 * i + 3]);
     }
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float inv = row_inverse(top, sum);
   uint4 *dst = reinterpret_cast<uint4 *>(p.out + index * D + c0);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     dst[i] = make_uint4(pack_bf16(acc[8 * i] * inv, acc[8 * i + 1] * inv), pack_bf16(acc[8 * i + 2] * inv, acc[8 * i + 3] * inv),
                         pack_bf16(acc[8 * i + 4] * inv, acc[8 * i + 5] * inv), pack_bf16(acc[8 * i + 6] * inv, acc[8 * i + 7] * inv));
-  if (c0 == 0 && p.lse) p.lse[index] = sum == 0.f ? -INFINITY : (top - kPOffP + log2f(sum)) * 0.6931471805599453f;
+  if (c0 == 0 && p.lse) p.lse[index] = row_lse(top, sum, kPOffP);
 }
 
 size_t part_rows(const Kv4AttnLaunch &p) {  // rows of all parts

@@ -12,7 +12,8 @@ import oracle.kv4_oracle as K
 import perf.operators as operators
 import synthetic as W
 from tests.parity import require_gpu
-from tests.test_gpu_kv4 import (BF16, cu_of, dev, fill_cache, i32, make_cache, pair_bound, positions, rand_rows)
+from tests.test_gpu_kv4 import (BF16, U, cache_rows, cu_of, dev, fill_cache, i32, make_cache, pair_bound, positions,
+                                rand_rows)
 
 pytestmark = pytest.mark.gpu
 
@@ -113,3 +114,74 @@ def test_measured_append_returns_what_its_plain_form_does(dtype, monkeypatch):
         got = operators.run(operators.prepare(case, 1))
         kinds.append({n: (t.dtype, tuple(t.shape)) for n, t in got.items()})
     assert kinds[0] == kinds[1]
+
+
+# ---------------------------------------------------------------- rows without a finite score
+
+FORMS = [  # dim, query heads, new tokens, first position, more pages than the context has: a step, drafts, a prompt
+    (64, 4, 1, 700, 0),
+    (64, 4, 4, 700, 700),
+    (128, 8, 1, 700, 0),
+    (128, 8, 1, 700, 1000),
+    (128, 8, 1, 30000, 0),
+    (128, 8, 1, 30000, 1000),
+    (128, 2, 4, 700, 1000),
+    (128, 4, 300, 700, 0),
+    (128, 4, 300, 9000, 0),
+    (64, 4, 300, 700, 0),
+    (64, 4, 300, 9000, 0),
+]
+
+
+@pytest.mark.parametrize("D,Hq,new,start,extra", FORMS)
+def test_rows_without_a_finite_score(D, Hq, new, start, extra):
+    """NaN wherever such a row sees a position, and zero and lse -inf only where it sees none, in every form."""
+    require_gpu()
+    rng = np.random.default_rng(D + new)
+    lens, starts = [new], [start]
+    c = make_cache(rng, lens, starts, 1, D, extra_blocks=extra)
+    n = start + new
+    k = torch.randn((n, 1, D), device="cuda")
+    k[:, 0, 5], k[:, 0, 40] = 3.0, 49152.0  # channels whose products have one sign
+    v = torch.randn((n, 1, D), device="cuda")
+    dsv4.kv4_append(k, v, cu_of([n]), i32([0]), c, rope_dims=0)
+    q, _ = rand_rows(rng, new, Hq, D, torch.bfloat16)
+    q[..., 40] = 0
+    run = lambda x, cache=c: dsv4.kv4_attention(x, cu_of(lens), i32(starts), cache, max_new=new, with_lse=True)
+    clean, lse0 = run(q)
+    gone = dsv4.DeviceKv4Cache(c.k_codes, c.v_codes, c.k_scales, c.v_scales, torch.full_like(c.block_table, -1))
+    at = new // 2
+    for channel, value in ((5, float("-inf")), (5, float("inf")), (5, float("nan")), (40, -3e38), (40, 3e38)):
+        bad = q.clone()
+        bad[at, 1] = 0
+        bad[at, 1, channel] = value
+        out, lse = run(bad)
+        assert out[at, 1].isnan().all() and lse[at, 1].isnan(), (channel, value)
+        out[at, 1], lse[at, 1] = clean[at, 1], lse0[at, 1]
+        assert torch.equal(out, clean) and torch.equal(lse, lse0)
+        out, lse = run(bad, gone)
+        assert torch.all(out == 0) and torch.all(lse == -np.inf), (channel, value)
+
+
+@pytest.mark.parametrize("D,Hq,new,start,extra", FORMS)
+def test_scores_below_float32_beside_others(D, Hq, new, start, extra):
+    """Positions whose scores leave float32's range downwards weigh nothing; the others decide."""
+    require_gpu()
+    rng = np.random.default_rng(D + new + 1)
+    c = make_cache(rng, [new], [start], 1, D, extra_blocks=extra)
+    n = start + new
+    k = torch.zeros((n, 1, D), device="cuda")
+    seen = [3, 131, n - new]  # the only ones in range
+    k[:, 0, 40] = 49152.0
+    k[seen, 0, 40] = 0
+    v = torch.randn((n, 1, D), device="cuda")
+    dsv4.kv4_append(k, v, cu_of([n]), i32([0]), c, rope_dims=0)
+    q = torch.zeros((new, Hq, D), device="cuda", dtype=torch.bfloat16)
+    q[..., 40] = -3e38
+    out, lse = dsv4.kv4_attention(q, cu_of([new]), i32([start]), c, max_new=new, with_lse=True)
+    _, vv = cache_rows(c, 0, n)
+    want = vv[seen].mean(0)[0]
+    # three equal weights, powers of two before they are divided by their sum
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= (BF16 + 8 * U) * np.abs(vv[seen]).mean(0)[0])
+    assert np.all(np.abs(lse.double().cpu().numpy() - np.log(3.0)) <= 2.0 ** -20)
+
