@@ -36,6 +36,8 @@
 // A value block with scale 255 (NaN) counts as zero in the product; the smallest such position is
 // noted per block of channels and rows that see it become NaN at the end, so that a row for which
 // the position is masked is not touched by it.
+#include <type_traits>
+
 #include "kv4_device.cuh"
 
 namespace dsv4 {
@@ -676,7 +678,10 @@ __global__ void __launch_bounds__(kThreadsA, StepShape<D, NT>::kResident)
 // the 128-row side, whose sums the block's scale multiplies afterwards:
 //   s_j = sum_b 2^k_jb (sum_c code_jc q_c)          8 x 4 scales a key in place of 128 conversions and products
 // q enters as two e4m3 values, hi + lo / 32, that hold its 8 bits exactly but for elements 2^-14 below the row's
-// largest, which are off by at most 2^-22 of that: columns 0-7 are the rows' hi and 8-15 their lo.
+// largest, which are off by at most 2^-22 of that: columns 0-7 are the rows' hi and 8-15 their lo. What is
+// missing is kept, and where it could move a score of the tile by more than kTcLoose, going by the keys' largest
+// scale, its products with the keys are added in float32 (tc_missing), so that no channel drowns beside a larger one.
+// On ordinary rows that never happens: the bound is some 2^-20 there.
 // Warp 4 brings keys (TMA, which spreads the codes to the operand's layout) and values (bulk copies) into two stages
 // each and issues the products; warps 0-3 take 32 keys of each tile, one per lane: scales, weights, and P to shared
 // memory, from where it is the B operand of mma.sync with the values as in the kernel above.
@@ -695,6 +700,7 @@ constexpr int kTcCols = 128;       // TMEM columns: two tiles of 4 blocks x 16
 constexpr float kTcOff = 7.f;      // weights are held times 2^7
 constexpr float kTcRaise = 8.f;
 constexpr float kTcNone = -kLeast;  // off of a row without a reference yet
+constexpr float kTcLoose = 6.1e-5f; // log2 that a score may be off by: an eighth of the weights' rounding to fp16
 
 struct alignas(1024) TcStepSmem {
   uint8_t k[2][kTcKeys * 128];     // codes, spread: 16 of them in each 16 bytes
@@ -711,6 +717,7 @@ struct alignas(1024) TcStepSmem {
   float2 ml[kWarps][8];
   float keep[kWarps][8];
   alignas(16) float rs[8];         // log2 score per product
+  alignas(16) float missing[8];    // log2 that a score is off by at most, at a scale of 1
   alignas(16) int lim[8];
   int64_t index[8];
   int64_t warp_sums[kTcThreads / 32];
@@ -723,6 +730,38 @@ struct alignas(1024) TcStepSmem {
 
 __device__ __forceinline__ int tc_seen(const Walk &u) {
   return max(min(u.stop(), (u.unit_limit() + kTcKeys - 1) / kTcKeys) - u.tile, 0);
+}
+
+// Adds the products of a key (one per lane) with what hi + lo / 32 leaves out of each row, which lies where warp 0's sums
+// will be: row tile r's channels 8 c .. 8 c + 7 at 16-byte word 16 r + c, bf16 (a remainder of 8 bits: exact).
+__device__ __forceinline__ void tc_missing(const Kv4AttnLaunch &p, const TcStepSmem &S, int64_t row, uint32_t scales,
+                                           uint64_t (&s)[4]) {
+  const uint4 *rest = reinterpret_cast<const uint4 *>(S.o[0]);
+  const uint32_t *codes = reinterpret_cast<const uint32_t *>(p.cache.k_codes + row * 64);
+#pragma unroll 1
+  for (int c = 0; c < 16; ++c) {
+    uint32_t h[4];
+    e2m1x8_to_half2(codes[c], h);
+    const uint32_t byte = scales >> (c / 4 * 8) & 255u;
+    const float f = byte > 127u + kKv4ExpMax ? 0.f : __uint_as_float(byte << 23);  // (a NaN block, or behind the last position)
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+      x[2 * i] = v.x * f, x[2 * i + 1] = v.y * f;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint4 ra = rest[16 * (2 * k) + c], rb = rest[16 * (2 * k + 1) + c];
+      const uint32_t a[4] = {ra.x, ra.y, ra.z, ra.w}, b[4] = {rb.x, rb.y, rb.z, rb.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[k] = fma_f32x2(pack_f32x2(x[2 * i], x[2 * i]), pack_f32x2(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16)), s[k]);
+        s[k] = fma_f32x2(pack_f32x2(x[2 * i + 1], x[2 * i + 1]),
+                         pack_f32x2(__uint_as_float(a[i] & 0xFFFF0000u), __uint_as_float(b[i] & 0xFFFF0000u)), s[k]);
+      }
+    }
+  }
 }
 
 // copies and products of the slice; w at its start
@@ -865,7 +904,8 @@ __device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Wa
       const int ex = static_cast<int>(am >> 23) - 127;
       const int sh = (am == 0 || ex >= 128) ? 0 : min(max(7 - ex, -120), 120);
       const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-      uint32_t hi[4], lo[4];
+      uint32_t hi[4], lo[4], rest[4];
+      float missing = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float a = __uint_as_float(x[k] << 16) * up, b = __uint_as_float(x[k] & 0xFFFF0000u) * up;
@@ -874,15 +914,23 @@ __device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Wa
         float la, lb;
         lo[k] = e4m3_pair((a - ha) * 32.f, (b - hb) * 32.f, la, lb);
         if (ex >= 128) hi[k] = lo[k] = 0x7F7Fu;
+        const float ra = ex >= 128 ? 0.f : fmaf(la, -0.03125f, a - ha), rb = ex >= 128 ? 0.f : fmaf(lb, -0.03125f, b - hb);
+        rest[k] = __byte_perm(__float_as_uint(ra), __float_as_uint(rb), 0x7632);
+        missing += fabsf(ra) + fabsf(rb);
       }
+#pragma unroll
+      for (int o2 = 1; o2 < 16; o2 <<= 1) missing += __shfl_xor_sync(0xFFFFFFFFu, missing, o2);
+      reinterpret_cast<uint4 *>(S.o[0])[tid] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
       const uint32_t at = sw128_offset(r, c >> 1) + 8 * (c & 1);
       *reinterpret_cast<uint2 *>(S.q + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
       *reinterpret_cast<uint2 *>(S.q + 1024 + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
       if (c == 0) {
         S.lim[r] = there ? min(w.q.n, w.q.start + static_cast<int>(i) + 1) : 0;
         S.index[r] = tok * p.Hq + head;
-        S.rs[r] = fmaxf(p.softmax_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23),
-                        1.17549435e-38f);
+        const float rs = fmaxf(p.softmax_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23),
+                               1.17549435e-38f);
+        S.rs[r] = rs;
+        S.missing[r] = 6.f * missing * rs;  // (6: the largest code)
       }
       if (tid < D / kKv4Block) S.nan_at[tid] = 0x7FFFFFFF;
     }
@@ -895,6 +943,14 @@ __device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Wa
       const int x = S.lim[r];
       if (x > 0) least = min(least, x);
     }
+    // 2^(byte - 127) * missing is above kTcLoose where the byte is above 104 + 127 - wide: the sum of a scale byte (104 to
+    // 140) less 104 and `wide` then has its upper bit. Four bytes at once.
+    // (Bytes behind the last position may be anything, and then it may too: what is added there is masked.)
+    float missing = 0.f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) missing = fmaxf(missing, S.missing[r]);
+    const int wide = min(max(104 + 127 - static_cast<int>(__float_as_uint(kTcLoose / missing) >> 23), 0), 128);
+    const uint32_t wide4 = static_cast<uint32_t>(wide - 104) * 0x01010101u;
     float o[KS][4];
     uint64_t off[R / 2], l[R / 2];  // per pair of rows: kTcOff - reference; this lane's sums
 #pragma unroll
@@ -902,152 +958,168 @@ __device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Wa
 #pragma unroll
     for (int k = 0; k < R / 2; ++k) off[k] = pack_f32x2(kTcNone, kTcNone), l[k] = 0;
 
-    for (int i = 0; i < count; ++i, ++n) {
-      const uint32_t slot = n & 1;
-      wait(&S.v_full[slot], n >> 1);
-      wait(&S.s_full[slot], n >> 1);
-      if (dead) break;
-      tc_fence_after();
-      const TcStepSmem::Values &T = S.v[slot];
-      const bool bad = S.bad[slot];
-      const int key0 = (w.tile + i) * kTcKeys + 32 * warp;  // the warp's first key
-      const bool edge = key0 + 32 > least;
-      const uint32_t kb = *reinterpret_cast<const uint32_t *>(T.ks + 4 * (32 * warp + lane));
-      uint32_t vb = *reinterpret_cast<const uint32_t *>(T.vs + 4 * (32 * warp + lane));
-      if ((edge || bad) && (bad || key0 + lane >= limit)) vb = 0;  // not a position of the unit
-      if (vb & vb << 1 & 0x80808080u) {  // no scale but NaN's byte has its two upper bits
+    // The tiles from the i-th on: all (`exact`: with what the products leave out), or those before the first that needs that.
+    // (As a branch in one loop it split a tile's code and took 3% of the time.)
+    int i = 0;
+    auto tiles = [&](auto exact) {
+      for (; i < count; ++i, ++n) {
+        const uint32_t slot = n & 1;
+        wait(&S.v_full[slot], n >> 1);
+        wait(&S.s_full[slot], n >> 1);
+        if (dead) break;
+        tc_fence_after();
+        const TcStepSmem::Values &T = S.v[slot];
+        const bool bad = S.bad[slot];
+        const int key0 = (w.tile + i) * kTcKeys + 32 * warp;  // the warp's first key
+        const bool edge = key0 + 32 > least;
+        const uint32_t kb = *reinterpret_cast<const uint32_t *>(T.ks + 4 * (32 * warp + lane));
+        if (!decltype(exact)::value && __any_sync(0xFFFFFFFFu, (kb + wide4) & 0x80808080u)) break;
+        uint32_t vb = *reinterpret_cast<const uint32_t *>(T.vs + 4 * (32 * warp + lane));
+        if ((edge || bad) && (bad || key0 + lane >= limit)) vb = 0;  // not a position of the unit
+        if (vb & vb << 1 & 0x80808080u) {  // no scale but NaN's byte has its two upper bits
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if ((vb >> (8 * b) & 255u) == 255u) {
-            atomicMin(&S.nan_at[b], key0 + lane);
-            vb &= ~(255u << (8 * b));
+          for (int b = 0; b < 4; ++b)
+            if ((vb >> (8 * b) & 255u) == 255u) {
+              atomicMin(&S.nan_at[b], key0 + lane);
+              vb &= ~(255u << (8 * b));
+            }
+        }
+        {
+          auto power = [&](int b) { return __uint_as_float((vb >> (8 * b) & 255u) << 23); };
+          const uint32_t h01 = pack_half2(power(0), power(1)), h23 = pack_half2(power(2), power(3));
+          sv_to[0] = static_cast<uint16_t>(h01), sv_to[32] = static_cast<uint16_t>(h01 >> 16);
+          sv_to[64] = static_cast<uint16_t>(h23), sv_to[96] = static_cast<uint16_t>(h23 >> 16);
+        }
+        const uint32_t s_at = tmem + 64 * slot + (static_cast<uint32_t>(32 * warp) << 16);
+        uint64_t s[R / 2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a[32];
+          tmem_ld32(s_at + 32 * h, a);
+          tmem_ld_wait();
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const float f = __uint_as_float((kb >> (8 * (2 * h + b)) & 255u) << 23);
+            const uint64_t f2 = pack_f32x2(f, f), part = pack_f32x2(0.03125f, 0.03125f);
+#pragma unroll
+            for (int k = 0; k < R / 2; ++k) {
+              const uint64_t hi = pack_f32x2(__uint_as_float(a[16 * b + 2 * k]), __uint_as_float(a[16 * b + 2 * k + 1]));
+              const uint64_t lo = pack_f32x2(__uint_as_float(a[16 * b + 8 + 2 * k]), __uint_as_float(a[16 * b + 9 + 2 * k]));
+              const uint64_t x = fma_f32x2(lo, part, hi);
+              s[k] = h + b == 0 ? mul_f32x2(f2, x) : fma_f32x2(f2, x, s[k]);
+            }
           }
-      }
-      {
-        auto power = [&](int b) { return __uint_as_float((vb >> (8 * b) & 255u) << 23); };
-        const uint32_t h01 = pack_half2(power(0), power(1)), h23 = pack_half2(power(2), power(3));
-        sv_to[0] = static_cast<uint16_t>(h01), sv_to[32] = static_cast<uint16_t>(h01 >> 16);
-        sv_to[64] = static_cast<uint16_t>(h23), sv_to[96] = static_cast<uint16_t>(h23 >> 16);
-      }
-      const uint32_t s_at = tmem + 64 * slot + (static_cast<uint32_t>(32 * warp) << 16);
-      uint64_t s[R / 2];
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.s_free[slot]);
+        if constexpr (decltype(exact)::value) {
+          if (!bad) {
+            constexpr int kPer = DSV4_PAGE_POSITIONS / kTcKeys;  // tiles of a page
+            const int t = w.tile + i, page = p.cache.block_table[static_cast<int64_t>(w.s) * p.cache.max_blocks + t / kPer];
+            const int64_t head = static_cast<int64_t>(page) * p.Hk + w.kvh;
+            tc_missing(p, S, head * DSV4_PAGE_POSITIONS + t % kPer * kTcKeys + 32 * warp + lane, kb, s);
+          }
+        }
+        if (kb & kb << 1 & 0x80808080u) {  // a NaN block makes the key's scores NaN
+          bool nan = false;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t a[32];
-        tmem_ld32(s_at + 32 * h, a);
-        tmem_ld_wait();
+          for (int b = 0; b < 4; ++b) nan |= (kb >> (8 * b) & 255u) == 255u;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const float f = __uint_as_float((kb >> (8 * (2 * h + b)) & 255u) << 23);
-          const uint64_t f2 = pack_f32x2(f, f), part = pack_f32x2(0.03125f, 0.03125f);
+          for (int k = 0; k < R / 2; ++k)
+            if (nan) s[k] = pack_f32x2(__uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u));
+        }
+        if (edge || bad) {
 #pragma unroll
           for (int k = 0; k < R / 2; ++k) {
-            const uint64_t hi = pack_f32x2(__uint_as_float(a[16 * b + 2 * k]), __uint_as_float(a[16 * b + 2 * k + 1]));
-            const uint64_t lo = pack_f32x2(__uint_as_float(a[16 * b + 8 + 2 * k]), __uint_as_float(a[16 * b + 9 + 2 * k]));
-            const uint64_t x = fma_f32x2(lo, part, hi);
-            s[k] = h + b == 0 ? mul_f32x2(f2, x) : fma_f32x2(f2, x, s[k]);
+            float a, b;
+            unpack_f32x2(s[k], a, b);
+            // (a row that is not there needs no mask, but for positions behind the last: its sums are not written)
+            const int la = S.lim[2 * k], lb = S.lim[2 * k + 1];
+            if (bad || key0 + lane >= (la > 0 ? la : limit)) a = -INFINITY;
+            if (bad || key0 + lane >= (lb > 0 ? lb : limit)) b = -INFINITY;
+            s[k] = pack_f32x2(a, b);
           }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.s_free[slot]);
-      if (kb & kb << 1 & 0x80808080u) {  // a NaN block makes the key's scores NaN
-        bool nan = false;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) nan |= (kb >> (8 * b) & 255u) == 255u;
-#pragma unroll
-        for (int k = 0; k < R / 2; ++k)
-          if (nan) s[k] = pack_f32x2(__uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u));
-      }
-      if (edge || bad) {
+        auto rs = [&](int k) { return *reinterpret_cast<const uint64_t *>(&S.rs[2 * k]); };
+        float y[R];
+        float most = -INFINITY;
 #pragma unroll
         for (int k = 0; k < R / 2; ++k) {
-          float a, b;
-          unpack_f32x2(s[k], a, b);
-          // (a row that is not there needs no mask, but for positions behind the last: its sums are not written)
-          const int la = S.lim[2 * k], lb = S.lim[2 * k + 1];
-          if (bad || key0 + lane >= (la > 0 ? la : limit)) a = -INFINITY;
-          if (bad || key0 + lane >= (lb > 0 ? lb : limit)) b = -INFINITY;
-          s[k] = pack_f32x2(a, b);
+          unpack_f32x2(fma_f32x2(s[k], rs(k), off[k]), y[2 * k], y[2 * k + 1]);
+          most = fmaxf(most, fmaxf(y[2 * k], y[2 * k + 1]));
         }
-      }
-      auto rs = [&](int k) { return *reinterpret_cast<const uint64_t *>(&S.rs[2 * k]); };
-      float y[R];
-      float most = -INFINITY;
+        if (__any_sync(0xFFFFFFFFu, most > kTcOff + kTcRaise)) {
 #pragma unroll
-      for (int k = 0; k < R / 2; ++k) {
-        unpack_f32x2(fma_f32x2(s[k], rs(k), off[k]), y[2 * k], y[2 * k + 1]);
-        most = fmaxf(most, fmaxf(y[2 * k], y[2 * k + 1]));
-      }
-      if (__any_sync(0xFFFFFFFFu, most > kTcOff + kTcRaise)) {
+          for (int k = 0; k < R / 2; ++k) {
+            float x[2], f[2], sums[2];
+            unpack_f32x2(mul_f32x2(s[k], rs(k)), x[0], x[1]);
+            unpack_f32x2(off[k], f[0], f[1]);
+            unpack_f32x2(l[k], sums[0], sums[1]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+              for (int o2 = 1; o2 < 32; o2 <<= 1) x[c] = fmaxf(x[c], __shfl_xor_sync(0xFFFFFFFFu, x[c], o2));
+              const float was = f[c] == kTcNone ? -kTcNone : kTcOff - f[c], now = fmaxf(was, ceilf(x[c]));
+              const float keep = now == was ? 1.f : ex2_approx(was - now);
+              if (now != was) f[c] = kTcOff - now;
+              sums[c] *= keep;
+              if (lane == 0) S.keep[warp][2 * k + c] = keep;
+            }
+            off[k] = pack_f32x2(f[0], f[1]);
+            l[k] = pack_f32x2(sums[0], sums[1]);
+            unpack_f32x2(fma_f32x2(s[k], rs(k), off[k]), y[2 * k], y[2 * k + 1]);
+          }
+          __syncwarp();
+          const float2 keep = *reinterpret_cast<const float2 *>(&S.keep[warp][2 * t4]);
+#pragma unroll
+          for (int k = 0; k < KS; ++k) o[k][0] *= keep.x, o[k][1] *= keep.y, o[k][2] *= keep.x, o[k][3] *= keep.y;
+          __syncwarp();
+        }
+        uint32_t h[R / 2];
 #pragma unroll
         for (int k = 0; k < R / 2; ++k) {
-          float x[2], f[2], sums[2];
-          unpack_f32x2(mul_f32x2(s[k], rs(k)), x[0], x[1]);
-          unpack_f32x2(off[k], f[0], f[1]);
-          unpack_f32x2(l[k], sums[0], sums[1]);
+          const float a = ex2_approx(y[2 * k]), b = ex2_approx(y[2 * k + 1]);
+          l[k] = add_f32x2(l[k], pack_f32x2(a, b));
+          h[k] = pack_half2(a, b);
+        }
+        S.pw[warp][lane] = make_uint4(h[0], h[1], h[2], h[3]);
+        __syncwarp();
+        uint32_t pb[4];
+        ldmatrix4_trans(pb, pw_at);
+        const uint4 sv = *reinterpret_cast<const uint4 *>(S.sv[warp][g >> 1][t4]);
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const int kA = 16 * mt + key_of(2 * t4), kB = 16 * mt + key_of(2 * t4 + 1);  // of the warp's 32
+          uint32_t c4[4][2];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int key = 32 * warp + ((q & 1) ? kB : kA) + (q >> 1) * 8;
+            const uint2 v = *reinterpret_cast<const uint2 *>(T.c + key * 64 + g * 8);
+            c4[q][0] = v.x, c4[q][1] = v.y;
+          }
+          const uint32_t sAB = mt == 0 ? sv.x : sv.z, sCD = mt == 0 ? sv.y : sv.w;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
+            uint32_t lo[2][4], hi[2][4];  // as in the kernel above
 #pragma unroll
-            for (int o2 = 1; o2 < 32; o2 <<= 1) x[c] = fmaxf(x[c], __shfl_xor_sync(0xFFFFFFFFu, x[c], o2));
-            const float was = f[c] == kTcNone ? -kTcNone : kTcOff - f[c], now = fmaxf(was, ceilf(x[c]));
-            const float keep = now == was ? 1.f : ex2_approx(was - now);
-            if (now != was) f[c] = kTcOff - now;
-            sums[c] *= keep;
-            if (lane == 0) S.keep[warp][2 * k + c] = keep;
+            for (int q = 0; q < 2; ++q) {
+              const uint32_t x = c4[2 * q][c], z = c4[2 * q + 1][c];
+              e2m1x8_to_half2((x & 0x0F0F0F0Fu) | (z << 4 & 0xF0F0F0F0u), lo[q]);
+              e2m1x8_to_half2((x >> 4 & 0x0F0F0F0Fu) | (z & 0xF0F0F0F0u), hi[q]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma16816(o[4 * c + k], hmul2(lo[0][k], sAB), hmul2(hi[0][k], sAB), hmul2(lo[1][k], sCD), hmul2(hi[1][k], sCD),
+                       pb[2 * mt], pb[2 * mt + 1]);
           }
-          off[k] = pack_f32x2(f[0], f[1]);
-          l[k] = pack_f32x2(sums[0], sums[1]);
-          unpack_f32x2(fma_f32x2(s[k], rs(k), off[k]), y[2 * k], y[2 * k + 1]);
         }
         __syncwarp();
-        const float2 keep = *reinterpret_cast<const float2 *>(&S.keep[warp][2 * t4]);
-#pragma unroll
-        for (int k = 0; k < KS; ++k) o[k][0] *= keep.x, o[k][1] *= keep.y, o[k][2] *= keep.x, o[k][3] *= keep.y;
-        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.v_free[slot]);
       }
-      uint32_t h[R / 2];
-#pragma unroll
-      for (int k = 0; k < R / 2; ++k) {
-        const float a = ex2_approx(y[2 * k]), b = ex2_approx(y[2 * k + 1]);
-        l[k] = add_f32x2(l[k], pack_f32x2(a, b));
-        h[k] = pack_half2(a, b);
-      }
-      S.pw[warp][lane] = make_uint4(h[0], h[1], h[2], h[3]);
-      __syncwarp();
-      uint32_t pb[4];
-      ldmatrix4_trans(pb, pw_at);
-      const uint4 sv = *reinterpret_cast<const uint4 *>(S.sv[warp][g >> 1][t4]);
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const int kA = 16 * mt + key_of(2 * t4), kB = 16 * mt + key_of(2 * t4 + 1);  // of the warp's 32
-        uint32_t c4[4][2];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int key = 32 * warp + ((q & 1) ? kB : kA) + (q >> 1) * 8;
-          const uint2 v = *reinterpret_cast<const uint2 *>(T.c + key * 64 + g * 8);
-          c4[q][0] = v.x, c4[q][1] = v.y;
-        }
-        const uint32_t sAB = mt == 0 ? sv.x : sv.z, sCD = mt == 0 ? sv.y : sv.w;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t lo[2][4], hi[2][4];  // as in the kernel above
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const uint32_t x = c4[2 * q][c], z = c4[2 * q + 1][c];
-            e2m1x8_to_half2((x & 0x0F0F0F0Fu) | (z << 4 & 0xF0F0F0F0u), lo[q]);
-            e2m1x8_to_half2((x >> 4 & 0x0F0F0F0Fu) | (z & 0xF0F0F0F0u), hi[q]);
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma16816(o[4 * c + k], hmul2(lo[0][k], sAB), hmul2(hi[0][k], sAB), hmul2(lo[1][k], sCD), hmul2(hi[1][k], sCD),
-                     pb[2 * mt], pb[2 * mt + 1]);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.v_free[slot]);
-    }
+    };
+    tiles(std::false_type{});
+    if (i < count && !dead) tiles(std::true_type{});
 #pragma unroll
     for (int k = 0; k < R / 2; ++k) {
       float f[2], sums[2];
@@ -1061,6 +1133,7 @@ __device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Wa
         if (lane == 0) S.ml[warp][2 * k + c] = make_float2(f[c] == kTcNone ? -INFINITY : kPOff - f[c], sums[c]);
       }
     }
+    named_bar_sync(1, 32 * kWarps);  // (all have read what the products leave out: warp 0's sums take its place)
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll

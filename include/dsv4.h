@@ -538,6 +538,7 @@ dsv4_status dsv4_kv4_append(const dsv4_kv4_append_args *args, dsv4_stream stream
  * and lse -inf. A NaN in a key or value makes NaN of the rows that see it and of no other. A query
  * with an infinity or a NaN makes NaN of its own row, out and lse, where that row sees any position.
  * Scores are float32: a row with one above its range, or with all of them below it, is NaN too.
+ * Elements of a query count to 2^-39 of its largest, in every form.
  * Workspace: dsv4_kv4_attention_workspace_size() bytes (of the sizes alone: q, out and lse may be
  * NULL there), 256-byte aligned; what it holds does not matter before the call or after it.
  */

@@ -185,3 +185,81 @@ def test_scores_below_float32_beside_others(D, Hq, new, start, extra):
     assert np.all(np.abs(out.double().cpu().numpy() - want) <= (BF16 + 8 * U) * np.abs(vv[seen]).mean(0)[0])
     assert np.all(np.abs(lse.double().cpu().numpy() - np.log(3.0)) <= 2.0 ** -20)
 
+
+
+# ---------------------------------------------------------------- rows of q with channels far above the others
+
+@pytest.mark.parametrize("extra", [0, 1000])  # more pages than the context has: both forms of a step
+@pytest.mark.parametrize("start", [700, 20000])
+@pytest.mark.parametrize("power", [12, 14, 18, 30, 60])
+def test_small_channels_beside_a_large_one(power, start, extra):
+    """Channels that are 2^-12 to 2^-60 of the row's largest decide where the keys are zero in that one. A score may be off by 2^-14
+    (of log2) more than at the head of test_gpu_kv4.py: where the form with scores on the tensor cores (wide tables) leaves out
+    more than that of a row, it adds it.
+
+    The form for narrow tables holds q in fp16, the row's largest element at 2^14 or more. Below fp16's normal numbers the step is 2^-24:
+    an element is off by at most half of it, 2^-25, which is 2^-39 of the largest, and a score by scale * 2^-39 * max |q| * sum |k|."""
+    require_gpu()
+    rng = np.random.default_rng(power + extra)
+    D, Hq, n = 128, 8, start + 1
+    c = make_cache(rng, [1], [start], 1, D, extra_blocks=extra)
+    large = [5, 37, 77, 127, 5, 64, 0]  # of each row but the last, which has none
+    k, v = (torch.randn((n, 1, D), device="cuda") for _ in range(2))
+    k[..., large] = 0
+    k[1, 0, 77] = 0.5 * 2.0 ** -power  # (a position where one of them counts as much as the others)
+    dsv4.kv4_append(k, v, cu_of([n]), i32([0]), c, rope_dims=0)
+    q = torch.randn((1, Hq, D), device="cuda")
+    for r, ch in enumerate(large):
+        q[0, r, ch] = 2.0 ** power
+    q = q.bfloat16()
+    kk, vv = cache_rows(c, 0, n)
+    for scale in (D ** -0.5, 1.0):
+        out, lse = dsv4.kv4_attention(q, cu_of([1]), i32([start]), c, max_new=1, softmax_scale=scale, with_lse=True)
+        want, wl, mag, top = K.attention(q.double().cpu().numpy(), kk, vv, start, scale)
+        eps = 2 * (D + 4) * U * top + 2.0 ** -21 + 2 * U * 1.4427 * (top + np.abs(wl)) + 2.0 ** -14 * np.log(2)
+        if extra == 0:
+            eps = eps + scale * 2.0 ** -39 * q.double().abs().amax(-1).cpu().numpy() * np.abs(kk).sum(-1).max()
+        limit = (2.0 ** -11 + 2 * eps[..., None]) * mag + 2.0 ** -32 * np.abs(vv).sum(0) + BF16 * np.abs(want)
+        assert np.all(np.abs(out.double().cpu().numpy() - want) <= limit)
+        assert np.all(np.abs(lse.double().cpu().numpy() - wl) <= eps + 4 * U * np.abs(wl) + 2.0 ** -21)
+
+
+@pytest.mark.parametrize("fill", [0xFF, 0xC8])
+@pytest.mark.parametrize("Hq,lens,starts", [(4, [2, 1], [250, 700]), (8, [1, 1], [0, 127]), (2, [3, 0, 4], [126, 5, 509])])
+def test_small_channels_under_masks_and_missing_pages(Hq, lens, starts, fill):
+    """The same beside positions that are masked, hold no values yet (NaN, or scales beyond fp16) or lie on a page that does not exist."""
+    require_gpu()
+    rng = np.random.default_rng(Hq + fill)
+    D = 128
+    c = make_cache(rng, lens, starts, 1, D, fill=fill, extra_blocks=700)
+    tot = [n + s for n, s in zip(lens, starts)]
+    k, v = (torch.randn((sum(tot), 1, D), device="cuda") for _ in range(2))
+    k[..., [7, 90]] = 0
+    dsv4.kv4_append(k, v, cu_of(tot), i32([0] * len(tot)), c, rope_dims=0)
+    q = torch.randn((sum(lens), Hq, D), device="cuda")
+    q[::2, :, 7] = 2.0 ** 18
+    q[1::2, 1, 90] = -2.0 ** 20
+    q = q.bfloat16()
+    rows = [cache_rows(c, s, n) for s, n in enumerate(tot)]
+    last = len(lens) - 1
+    for gone in (False, True):
+        table = c.block_table.clone()
+        if gone:
+            table[last, 0] = -1
+        cache = dsv4.DeviceKv4Cache(c.k_codes, c.v_codes, c.k_scales, c.v_scales, table)
+        out, lse = dsv4.kv4_attention(q, cu_of(lens), i32(starts), cache, max_new=max(lens), softmax_scale=1.0, with_lse=True)
+        at = 0
+        for s, (n, first) in enumerate(zip(lens, starts)):
+            for i in range(n):
+                keep = [j for j in range(first + i + 1) if not (gone and s == last and j < 256)]
+                got, gl = out[at + i].double().cpu().numpy(), lse[at + i].double().cpu().numpy()
+                if not keep:
+                    assert np.all(got == 0) and np.all(gl == -np.inf)
+                    continue
+                kk, vv = rows[s][0][keep], rows[s][1][keep]
+                want, wl, mag, top = K.attention(q[at + i:at + i + 1].double().cpu().numpy(), kk, vv, len(keep) - 1, 1.0)
+                eps = 2 * (D + 4) * U * top + 2.0 ** -21 + 2 * U * 1.4427 * (top + np.abs(wl)) + 2.0 ** -14 * np.log(2)
+                limit = (2.0 ** -11 + 2 * eps[..., None]) * mag + 2.0 ** -32 * np.abs(vv).sum(0) + BF16 * np.abs(want)
+                assert np.all(np.abs(got - want[0]) <= limit[0])
+                assert np.all(np.abs(gl - wl[0]) <= (eps + 4 * U * np.abs(wl) + 2.0 ** -21)[0])
+            at += n
