@@ -109,6 +109,13 @@ class Kv4AttentionArgs(C.Structure):
                 ("softmax_scale", C.c_float), ("out", p), ("lse", p), ("d_status", p)]
 
 
+KV4_STEP, KV4_STEP_TENSOR, KV4_PROMPT = range(3)
+
+
+class Kv4Plan(C.Structure):
+    _fields_ = [("form", i32), ("rows", i32), ("units", i32), ("shared", i32), ("splits", i32)]
+
+
 EXPORTS = {
     "dsv4_compress": (C.c_int, [C.POINTER(CompressArgs), p]),
     "dsv4_compress_project_workspace_size": (C.c_size_t, [C.POINTER(CompressProjectArgs)]),
@@ -125,6 +132,7 @@ EXPORTS = {
     "dsv4_qk_norm_rope": (C.c_int, [C.POINTER(QkNormRopeArgs), p]),
     "dsv4_kv4_append": (C.c_int, [C.POINTER(Kv4AppendArgs), p]),
     "dsv4_kv4_attention_workspace_size": (C.c_size_t, [C.POINTER(Kv4AttentionArgs)]),
+    "dsv4_kv4_attention_plan": (C.c_int, [C.POINTER(Kv4AttentionArgs), C.POINTER(Kv4Plan)]),
     "dsv4_kv4_attention": (C.c_int, [C.POINTER(Kv4AttentionArgs), p, C.c_size_t, p]),
     "dsv4_status_string": (C.c_char_p, [C.c_int]),
     "dsv4_abi_version": (i32, []),

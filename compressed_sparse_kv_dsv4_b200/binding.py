@@ -608,6 +608,14 @@ def kv4_attention_args(q, cu_seqlens, start_pos, cache: DeviceKv4Cache, *, max_n
                               _opt("lse", lse, _F32, q.shape[:2], dev), _status(d_status, dev))
 
 
+def kv4_attention_plan(args: A.Kv4AttentionArgs) -> A.Kv4Plan:
+    """Which kernel a kv4_attention call with these marshalled arguments takes (A.KV4_STEP, A.KV4_STEP_TENSOR or
+    A.KV4_PROMPT), the rows of its tiles and how a prompt's keys are shared out. Nothing is launched."""
+    plan = A.Kv4Plan()
+    A.check("dsv4_kv4_attention_plan", A.load().dsv4_kv4_attention_plan(C.byref(args), C.byref(plan)))
+    return plan
+
+
 def kv4_attention_workspace_size(args: A.Kv4AttentionArgs) -> int:
     """dsv4_kv4_attention_workspace_size for the marshalled arguments of a kv4_attention call."""
     return A.load().dsv4_kv4_attention_workspace_size(C.byref(args))

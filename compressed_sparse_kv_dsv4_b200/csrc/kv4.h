@@ -73,15 +73,23 @@ struct Kv4AttnLaunch {
   float *lse;               // [T][Hq] or null
   uint32_t *d_status;
 };
-size_t kv4_attention_workspace_bytes(const Kv4AttnLaunch &p);
-cudaError_t launch_kv4_attention(const Kv4AttnLaunch &p, void *ws, cudaStream_t st);
-// the form for many rows per sequence (launch_kv4_attention chooses)
+// how the form for many rows per sequence shares out a call
 struct Kv4PromptShape {
   int row_blocks;     // blocks of 256 rows of each sequence and key/value head
   int whole, splits;  // units that one CTA takes; CTAs of each of the others
 };
 Kv4PromptShape kv4_prompt_shape(const Kv4AttnLaunch &p);
-size_t kv4_prompt_workspace_bytes(const Kv4AttnLaunch &p);
-cudaError_t launch_kv4_prompt(const Kv4AttnLaunch &p, void *ws, cudaStream_t st);
+
+// which kernel takes a call: of sizes and the codes' alignment alone
+struct Kv4AttnPlan {
+  dsv4_kv4_form form;
+  int rows;              // of a row tile
+  Kv4PromptShape shape;  // DSV4_KV4_PROMPT
+};
+Kv4AttnPlan kv4_attention_plan(const Kv4AttnLaunch &p);
+size_t kv4_attention_workspace_bytes(const Kv4AttnLaunch &p, const Kv4AttnPlan &plan);
+cudaError_t launch_kv4_attention(const Kv4AttnLaunch &p, const Kv4AttnPlan &plan, void *ws, cudaStream_t st);
+size_t kv4_prompt_workspace_bytes(const Kv4AttnLaunch &p, const Kv4PromptShape &g);
+cudaError_t launch_kv4_prompt(const Kv4AttnLaunch &p, const Kv4PromptShape &g, void *ws, cudaStream_t st);
 
 }  // namespace dsv4

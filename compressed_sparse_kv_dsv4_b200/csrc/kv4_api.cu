@@ -168,7 +168,22 @@ dsv4_status dsv4_kv4_append(const dsv4_kv4_append_args *a, dsv4_stream stream) {
 size_t dsv4_kv4_attention_workspace_size(const dsv4_kv4_attention_args *a) {
   Kv4AttnLaunch p;
   if (attention_args(a, &p, false) != DSV4_OK) return 0;
-  return kv4_attention_workspace_bytes(p);
+  return kv4_attention_workspace_bytes(p, kv4_attention_plan(p));
+}
+
+dsv4_status dsv4_kv4_attention_plan(const dsv4_kv4_attention_args *a, dsv4_kv4_plan *out) {
+  Kv4AttnLaunch p;
+  if (!out) return DSV4_ERR_INVALID_ARG;
+  const dsv4_status s = attention_args(a, &p, false);
+  if (s != DSV4_OK) return s;
+  const Kv4AttnPlan plan = kv4_attention_plan(p);
+  const bool prompt = plan.form == DSV4_KV4_PROMPT;
+  out->form = plan.form;
+  out->rows = plan.rows;
+  out->units = prompt ? plan.shape.row_blocks * p.B * p.Hk : 0;
+  out->shared = prompt ? out->units - plan.shape.whole : 0;
+  out->splits = prompt ? plan.shape.splits : 0;
+  return DSV4_OK;
 }
 
 dsv4_status dsv4_kv4_attention(const dsv4_kv4_attention_args *a, void *ws, size_t ws_bytes, dsv4_stream stream) {
@@ -176,9 +191,10 @@ dsv4_status dsv4_kv4_attention(const dsv4_kv4_attention_args *a, void *ws, size_
   const dsv4_status s = attention_args(a, &p, true);
   if (s != DSV4_OK) return s;
   if (p.T == 0) return DSV4_OK;
-  if (!ws || ws_bytes < kv4_attention_workspace_bytes(p) || (reinterpret_cast<uintptr_t>(ws) & 255u))
+  const Kv4AttnPlan plan = kv4_attention_plan(p);
+  if (!ws || ws_bytes < kv4_attention_workspace_bytes(p, plan) || (reinterpret_cast<uintptr_t>(ws) & 255u))
     return DSV4_ERR_INVALID_ARG;
-  return to_status(launch_kv4_attention(p, ws, static_cast<cudaStream_t>(stream)));
+  return to_status(launch_kv4_attention(p, plan, ws, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

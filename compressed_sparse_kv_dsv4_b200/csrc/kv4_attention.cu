@@ -1291,7 +1291,7 @@ __global__ void __launch_bounds__(kCombineThreads, 8) kv4_combine_kernel(const _
 // there are 283 (409) row tiles to a wave. Measured beside that, at 8 key heads, of 4 query heads each, step form and
 // the other: 8 sequences of 32768 positions, 16 new tokens (256 row tiles) 384 us and 433 us, 32 (512) 747 us
 // and 437 us. Short contexts are latency: 24 us against 15 us for 16 rows and more at 512 positions.
-bool prompt_rows(const Kv4AttnLaunch &p) {
+bool prompt_rows(const Kv4AttnLaunch &p, const Kv4PromptShape &g) {
   const int64_t group = p.Hq / p.Hk, rows = (p.max_new < p.T ? p.max_new : p.T) * group;
   if (rows <= 8) return false;
   auto row_blocks = [&](int64_t size) {  // of `size` rows: at most what the longest sequence has of each, and what all tokens make
@@ -1300,7 +1300,6 @@ bool prompt_rows(const Kv4AttnLaunch &p) {
   };
   const int64_t sms = sm_count(), waves = (row_blocks(256) + sms - 1) / sms;
   if (p.cache.max_blocks <= 4 && waves <= 2) return true;
-  const Kv4PromptShape g = kv4_prompt_shape(p);
   return row_blocks(16) * (g.whole == 0 ? g.splits : 1) > (p.D == 128 ? 283 : 409) * waves;
 }
 
@@ -1318,7 +1317,6 @@ int tile_rows(const Kv4AttnLaunch &p) {
   const int64_t rows = (p.max_new < p.T ? p.max_new : p.T) * (p.Hq / p.Hk);
   return rows <= 8 || turns_of_8(p) < int64_t(8) * 12 * sm_count() ? 8 : 16;
 }
-int resident(const Kv4AttnLaunch &p) { return resident_ctas(p.D, tile_rows(p) / 8); }
 
 template <int D, int NT>
 cudaError_t launch_step(AttnParams &P, cudaStream_t st) {
@@ -1333,19 +1331,18 @@ cudaError_t launch_step(AttnParams &P, cudaStream_t st) {
 // heads each, the kernel above and this one: 8 sequences of 2000 positions (1024 tiles) 15.7 us and 20.0 us, one of
 // 32000 (2000) 21.4 us and 24.7 us; 64 of 500 (2048) 33.9 us and 26.8 us, 8 of 8000 (4096) 31.8 us and 28.8 us, 8 of
 // 32000 81.4 us and 70.4 us.
-bool tensor_scores(const Kv4AttnLaunch &p) {
-  return p.D == 128 && tile_rows(p) == 8 && turns_of_8(p) >= int64_t(4) * (kTcKeys / kTile) * kTcResident * sm_count();
+// Its tensor map wants the codes at a multiple of 32 bytes and rows that an int counts.
+bool tensor_scores(const Kv4AttnLaunch &p, int rows) {
+  return p.D == 128 && rows == 8 && turns_of_8(p) >= int64_t(4) * (kTcKeys / kTile) * kTcResident * sm_count() &&
+         static_cast<int64_t>(p.cache.num_pages) * p.Hk * DSV4_PAGE_POSITIONS <= 0x7FFFFFFF &&
+         reinterpret_cast<uintptr_t>(p.cache.k_codes) % 32 == 0;
 }
 
-// Its tensor map wants the codes at a multiple of 32 bytes and rows that
-// an int counts.
 bool make_codes_map(CUtensorMap *map, const Kv4AttnLaunch &p) {
-  const int64_t rows = static_cast<int64_t>(p.cache.num_pages) * p.Hk * DSV4_PAGE_POSITIONS;
-  if (rows > 0x7FFFFFFF || reinterpret_cast<uintptr_t>(p.cache.k_codes) % 32 != 0) return false;
   auto fn = get_encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(rows)};  // codes
-  const cuuint64_t strides[1] = {64};                               // bytes
+  const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(p.cache.num_pages) * p.Hk * DSV4_PAGE_POSITIONS};  // codes
+  const cuuint64_t strides[1] = {64};                                                                         // bytes
   const cuuint32_t box[2] = {128, kTcKeys}, steps[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, p.cache.k_codes, dims, strides, box, steps,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1361,27 +1358,41 @@ cudaError_t launch_tc_step(AttnParams &P, const CUtensorMap &map, cudaStream_t s
 
 }  // namespace
 
-size_t kv4_attention_workspace_bytes(const Kv4AttnLaunch &p) {
-  if (prompt_rows(p)) return align_up(kv4_prompt_workspace_bytes(p) + 1, 256);
-  const int R = tile_rows(p);
-  const size_t rows = static_cast<size_t>(sm_count()) * resident(p) * 2 * R;
+Kv4AttnPlan kv4_attention_plan(const Kv4AttnLaunch &p) {
+  Kv4AttnPlan plan{};
+  plan.shape = kv4_prompt_shape(p);
+  if (prompt_rows(p, plan.shape)) {
+    plan.form = DSV4_KV4_PROMPT;
+    plan.rows = 256;
+  } else {
+    plan.rows = tile_rows(p);
+    plan.form = tensor_scores(p, plan.rows) ? DSV4_KV4_STEP_TENSOR : DSV4_KV4_STEP;
+  }
+  return plan;
+}
+
+size_t kv4_attention_workspace_bytes(const Kv4AttnLaunch &p, const Kv4AttnPlan &plan) {
+  if (plan.form == DSV4_KV4_PROMPT) return align_up(kv4_prompt_workspace_bytes(p, plan.shape) + 1, 256);
+  const size_t rows = static_cast<size_t>(sm_count()) * resident_ctas(p.D, plan.rows / 8) * 2 * plan.rows;
   return align_up(rows * p.D * sizeof(float), 256) + align_up(rows * sizeof(float2), 256);
 }
 
-cudaError_t launch_kv4_attention(const Kv4AttnLaunch &q, void *ws, cudaStream_t st) {
-  if (prompt_rows(q)) return launch_kv4_prompt(q, ws, st);
+cudaError_t launch_kv4_attention(const Kv4AttnLaunch &q, const Kv4AttnPlan &plan, void *ws, cudaStream_t st) {
+  if (plan.form == DSV4_KV4_PROMPT) return launch_kv4_prompt(q, plan.shape, ws, st);
   AttnParams P{};
   P.a = q;
-  const int R = tile_rows(q);
-  CUtensorMap map;
-  const bool tc = tensor_scores(q) && make_codes_map(&map, q);
-  P.ctas = sm_count() * (tc ? kTcResident : resident(q));
+  const int R = plan.rows;
+  const bool tc = plan.form == DSV4_KV4_STEP_TENSOR;
+  P.ctas = sm_count() * (tc ? kTcResident : resident_ctas(q.D, R / 8));
   P.key_log2 = tc ? 7 : 6;
   P.group = q.Hq / q.Hk;
   P.part_o = static_cast<float *>(ws);
   P.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(ws) +
                                          align_up(static_cast<size_t>(P.ctas) * 2 * R * q.D * sizeof(float), 256));
-  if (tc) return launch_tc_step(P, map, st);
+  if (tc) {
+    CUtensorMap map;
+    return make_codes_map(&map, q) ? launch_tc_step(P, map, st) : cudaErrorNotSupported;
+  }
   if (q.D == 64) return R == 8 ? launch_step<64, 1>(P, st) : launch_step<64, 2>(P, st);
   return R == 8 ? launch_step<128, 1>(P, st) : launch_step<128, 2>(P, st);
 }

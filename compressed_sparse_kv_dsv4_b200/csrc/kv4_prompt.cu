@@ -608,8 +608,7 @@ __global__ void __launch_bounds__(kRows) kv4_prompt_combine_kernel(const __grid_
   if (c0 == 0 && p.lse) p.lse[index] = row_lse(top, sum, kPOffP);
 }
 
-size_t part_rows(const Kv4AttnLaunch &p) {  // rows of all parts
-  const Kv4PromptShape g = kv4_prompt_shape(p);
+size_t part_rows(const Kv4AttnLaunch &p, const Kv4PromptShape &g) {  // rows of all parts
   return (static_cast<size_t>(g.row_blocks) * p.B * p.Hk - g.whole) * g.splits * 2 * kRows;
 }
 
@@ -657,19 +656,19 @@ Kv4PromptShape kv4_prompt_shape(const Kv4AttnLaunch &p) {
   return g;
 }
 
-size_t kv4_prompt_workspace_bytes(const Kv4AttnLaunch &p) {
-  return align_up(part_rows(p) * p.D * sizeof(float), 256) + align_up(part_rows(p) * sizeof(float2), 256);
+size_t kv4_prompt_workspace_bytes(const Kv4AttnLaunch &p, const Kv4PromptShape &g) {
+  const size_t rows = part_rows(p, g);
+  return align_up(rows * p.D * sizeof(float), 256) + align_up(rows * sizeof(float2), 256);
 }
 
-cudaError_t launch_kv4_prompt(const Kv4AttnLaunch &q, void *ws, cudaStream_t st) {
+cudaError_t launch_kv4_prompt(const Kv4AttnLaunch &q, const Kv4PromptShape &g, void *ws, cudaStream_t st) {
   PromptParams P{};
   P.a = q;
-  const Kv4PromptShape g = kv4_prompt_shape(q);
   P.row_blocks = g.row_blocks;
   P.whole = g.whole;
   P.splits = g.splits;
   P.part_o = static_cast<float4 *>(ws);
-  P.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(ws) + align_up(part_rows(q) * q.D * sizeof(float), 256));
+  P.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(ws) + align_up(part_rows(q, g) * q.D * sizeof(float), 256));
   return q.D == 64 ? launch_typed<64>(P, st) : launch_typed<128>(P, st);
 }
 

@@ -559,6 +559,25 @@ typedef struct {
   uint32_t *d_status;
 } dsv4_kv4_attention_args;
 
+/*
+ * dsv4_kv4_attention_plan: how a call with these arguments is carried out, without making it (host
+ * only; q, out and lse may be NULL). It follows from max_new, total_tokens, batch, the heads, dim, the
+ * table's width (the longest context that it holds) and the alignment of k_codes.
+ *   DSV4_KV4_STEP         tiles of 8 or 16 rows (new tokens x query heads of a key/value head)
+ *   DSV4_KV4_STEP_TENSOR  tiles of 8 rows, scores on the tensor cores: dim 128, wide tables
+ *   DSV4_KV4_PROMPT       blocks of 256 rows; `units` blocks of all sequences and key/value heads, the keys of
+ *                         `shared` of them split over `splits` CTAs each
+ */
+typedef enum { DSV4_KV4_STEP = 0, DSV4_KV4_STEP_TENSOR = 1, DSV4_KV4_PROMPT = 2 } dsv4_kv4_form;
+
+typedef struct {
+  int32_t form; /* dsv4_kv4_form */
+  int32_t rows;
+  int32_t units, shared, splits; /* DSV4_KV4_PROMPT, otherwise 0 */
+} dsv4_kv4_plan;
+
+dsv4_status dsv4_kv4_attention_plan(const dsv4_kv4_attention_args *args, dsv4_kv4_plan *plan);
+
 size_t dsv4_kv4_attention_workspace_size(const dsv4_kv4_attention_args *args);
 dsv4_status dsv4_kv4_attention(const dsv4_kv4_attention_args *args, void *workspace, size_t workspace_bytes,
                                dsv4_stream stream);
