@@ -132,6 +132,7 @@ EXPORTS = {
     "dsv4_qk_norm_rope": (C.c_int, [C.POINTER(QkNormRopeArgs), p]),
     "dsv4_kv4_append": (C.c_int, [C.POINTER(Kv4AppendArgs), p]),
     "dsv4_kv4_attention_workspace_size": (C.c_size_t, [C.POINTER(Kv4AttentionArgs)]),
+    "dsv4_kv4_attention_workspace_limit": (C.c_size_t, [C.POINTER(Kv4AttentionArgs)]),
     "dsv4_kv4_attention_plan": (C.c_int, [C.POINTER(Kv4AttentionArgs), C.POINTER(Kv4Plan)]),
     "dsv4_kv4_attention": (C.c_int, [C.POINTER(Kv4AttentionArgs), p, C.c_size_t, p]),
     "dsv4_status_string": (C.c_char_p, [C.c_int]),

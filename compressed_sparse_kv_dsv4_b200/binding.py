@@ -616,15 +616,18 @@ def kv4_attention_plan(args: A.Kv4AttentionArgs) -> A.Kv4Plan:
     return plan
 
 
-def kv4_attention_workspace_size(args: A.Kv4AttentionArgs) -> int:
-    """dsv4_kv4_attention_workspace_size for the marshalled arguments of a kv4_attention call."""
-    return A.load().dsv4_kv4_attention_workspace_size(C.byref(args))
+def kv4_attention_workspace_size(args: A.Kv4AttentionArgs, smaller: bool = False) -> int:
+    """dsv4_kv4_attention_workspace_size for the marshalled arguments of a kv4_attention call; smaller: what every call
+    needs at most whose sequences, tokens, max_new and table width are no larger (dsv4_kv4_attention_workspace_limit)."""
+    lib = A.load()
+    return (lib.dsv4_kv4_attention_workspace_limit if smaller else lib.dsv4_kv4_attention_workspace_size)(C.byref(args))
 
 
-def kv4_attention_workspace(q, cu_seqlens, cache: DeviceKv4Cache, *, max_new: int) -> torch.Tensor:
-    """A workspace for kv4_attention calls of these sizes (one call at a time may use it)."""
+def kv4_attention_workspace(q, cu_seqlens, cache: DeviceKv4Cache, *, max_new: int, smaller: bool = False) -> torch.Tensor:
+    """A workspace for kv4_attention calls of these sizes (one call at a time may use it); smaller: also for every
+    call with fewer sequences or tokens, a smaller max_new or a narrower table, which may need more than this one."""
     with _elsewhere(q.get_device(), None) or contextlib.nullcontext():
-        n = kv4_attention_workspace_size(kv4_attention_args(q, cu_seqlens, cu_seqlens[:-1], cache, max_new=max_new))
+        n = kv4_attention_workspace_size(kv4_attention_args(q, cu_seqlens, cu_seqlens[:-1], cache, max_new=max_new), smaller)
         if n == 0:
             A.check("dsv4_kv4_attention_workspace_size", A.ERR_INVALID_ARG)
         return torch.empty(n, dtype=torch.uint8, device=q.device)

@@ -79,6 +79,7 @@ struct Kv4PromptShape {
   int whole, splits;  // units that one CTA takes; CTAs of each of the others
 };
 Kv4PromptShape kv4_prompt_shape(const Kv4AttnLaunch &p);
+int64_t kv4_prompt_most_parts(const Kv4AttnLaunch &p);  // of any call whose sizes are no larger
 
 // which kernel takes a call: of sizes and the codes' alignment alone
 struct Kv4AttnPlan {
@@ -88,8 +89,12 @@ struct Kv4AttnPlan {
 };
 Kv4AttnPlan kv4_attention_plan(const Kv4AttnLaunch &p);
 size_t kv4_attention_workspace_bytes(const Kv4AttnLaunch &p, const Kv4AttnPlan &plan);
+size_t kv4_attention_workspace_limit(const Kv4AttnLaunch &p);  // of any call whose sizes are no larger
 cudaError_t launch_kv4_attention(const Kv4AttnLaunch &p, const Kv4AttnPlan &plan, void *ws, cudaStream_t st);
-size_t kv4_prompt_workspace_bytes(const Kv4AttnLaunch &p, const Kv4PromptShape &g);
+size_t kv4_prompt_workspace_bytes(int dim, int64_t parts);  // parts: CTAs that share units
+inline int64_t kv4_prompt_parts(const Kv4AttnLaunch &p, const Kv4PromptShape &g) {
+  return (static_cast<int64_t>(g.row_blocks) * p.B * p.Hk - g.whole) * g.splits;
+}
 cudaError_t launch_kv4_prompt(const Kv4AttnLaunch &p, const Kv4PromptShape &g, void *ws, cudaStream_t st);
 
 }  // namespace dsv4

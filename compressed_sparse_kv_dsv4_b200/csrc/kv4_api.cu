@@ -171,6 +171,12 @@ size_t dsv4_kv4_attention_workspace_size(const dsv4_kv4_attention_args *a) {
   return kv4_attention_workspace_bytes(p, kv4_attention_plan(p));
 }
 
+size_t dsv4_kv4_attention_workspace_limit(const dsv4_kv4_attention_args *a) {
+  Kv4AttnLaunch p;
+  if (attention_args(a, &p, false) != DSV4_OK) return 0;
+  return kv4_attention_workspace_limit(p);
+}
+
 dsv4_status dsv4_kv4_attention_plan(const dsv4_kv4_attention_args *a, dsv4_kv4_plan *out) {
   Kv4AttnLaunch p;
   if (!out) return DSV4_ERR_INVALID_ARG;

@@ -1371,10 +1371,27 @@ Kv4AttnPlan kv4_attention_plan(const Kv4AttnLaunch &p) {
   return plan;
 }
 
+namespace {
+size_t step_workspace_bytes(int D, int R) {
+  const size_t rows = static_cast<size_t>(sm_count()) * resident_ctas(D, R / 8) * 2 * R;
+  return align_up(rows * D * sizeof(float), 256) + align_up(rows * sizeof(float2), 256);
+}
+size_t prompt_workspace_bytes(int D, int64_t parts) { return align_up(kv4_prompt_workspace_bytes(D, parts) + 1, 256); }
+}  // namespace
+
 size_t kv4_attention_workspace_bytes(const Kv4AttnLaunch &p, const Kv4AttnPlan &plan) {
-  if (plan.form == DSV4_KV4_PROMPT) return align_up(kv4_prompt_workspace_bytes(p, plan.shape) + 1, 256);
-  const size_t rows = static_cast<size_t>(sm_count()) * resident_ctas(p.D, plan.rows / 8) * 2 * plan.rows;
-  return align_up(rows * p.D * sizeof(float), 256) + align_up(rows * sizeof(float2), 256);
+  return plan.form == DSV4_KV4_PROMPT ? prompt_workspace_bytes(p.D, kv4_prompt_parts(p, plan.shape))
+                                      : step_workspace_bytes(p.D, plan.rows);
+}
+
+size_t kv4_attention_workspace_limit(const Kv4AttnLaunch &p) {
+  size_t most = step_workspace_bytes(p.D, 8);
+  if ((p.max_new < p.T ? p.max_new : p.T) * static_cast<int64_t>(p.Hq / p.Hk) > 8) {  // the other forms want more rows
+    const size_t step = step_workspace_bytes(p.D, 16), prompt = prompt_workspace_bytes(p.D, kv4_prompt_most_parts(p));
+    most = most > step ? most : step;
+    most = most > prompt ? most : prompt;
+  }
+  return most;
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnLaunch &q, const Kv4AttnPlan &plan, void *ws, cudaStream_t st) {

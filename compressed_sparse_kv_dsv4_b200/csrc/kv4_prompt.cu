@@ -608,10 +608,6 @@ __global__ void __launch_bounds__(kRows) kv4_prompt_combine_kernel(const __grid_
   if (c0 == 0 && p.lse) p.lse[index] = row_lse(top, sum, kPOffP);
 }
 
-size_t part_rows(const Kv4AttnLaunch &p, const Kv4PromptShape &g) {  // rows of all parts
-  return (static_cast<size_t>(g.row_blocks) * p.B * p.Hk - g.whole) * g.splits * 2 * kRows;
-}
-
 template <int D>
 cudaError_t launch_typed(const PromptParams &P, cudaStream_t st) {
   const size_t smem = sizeof(PromptSmem<D>) + 1024;
@@ -656,9 +652,20 @@ Kv4PromptShape kv4_prompt_shape(const Kv4AttnLaunch &p) {
   return g;
 }
 
-size_t kv4_prompt_workspace_bytes(const Kv4AttnLaunch &p, const Kv4PromptShape &g) {
-  const size_t rows = part_rows(p, g);
-  return align_up(rows * p.D * sizeof(float), 256) + align_up(rows * sizeof(float2), 256);
+// A call of no more units has as many parts at most: up to half the SMs' number of units, one wave; with more, as many
+// waves as `splits` CTAs a unit may take to be an eighth of a unit shorter than one, ceil(7/8 splits) - 1.
+int64_t kv4_prompt_most_parts(const Kv4AttnLaunch &p) {
+  const int64_t tiles = static_cast<int64_t>(p.cache.max_blocks) * (DSV4_PAGE_POSITIONS / kKeys), sms = sm_count();
+  const Kv4PromptShape g = kv4_prompt_shape(p);
+  int64_t parts = tiles >= 8 ? sms : 0;
+  if (static_cast<int64_t>(g.row_blocks) * p.B * p.Hk > sms)
+    for (int k = 2; k <= 8 && k <= tiles / 8; ++k) parts = ((7 * k + 7) / 8 - 1) * sms;
+  return parts;
+}
+
+size_t kv4_prompt_workspace_bytes(int dim, int64_t parts) {
+  const size_t rows = static_cast<size_t>(parts) * 2 * kRows;
+  return align_up(rows * dim * sizeof(float), 256) + align_up(rows * sizeof(float2), 256);
 }
 
 cudaError_t launch_kv4_prompt(const Kv4AttnLaunch &q, const Kv4PromptShape &g, void *ws, cudaStream_t st) {
@@ -668,7 +675,7 @@ cudaError_t launch_kv4_prompt(const Kv4AttnLaunch &q, const Kv4PromptShape &g, v
   P.whole = g.whole;
   P.splits = g.splits;
   P.part_o = static_cast<float4 *>(ws);
-  P.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(ws) + align_up(part_rows(q, g) * q.D * sizeof(float), 256));
+  P.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(ws) + align_up(static_cast<size_t>(kv4_prompt_parts(q, g)) * 2 * kRows * q.D * sizeof(float), 256));
   return q.D == 64 ? launch_typed<64>(P, st) : launch_typed<128>(P, st);
 }
 

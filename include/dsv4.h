@@ -540,7 +540,12 @@ dsv4_status dsv4_kv4_append(const dsv4_kv4_append_args *args, dsv4_stream stream
  * Scores are float32: a row with one above its range, or with all of them below it, is NaN too.
  * Elements of a query count to 2^-39 of its largest, in every form.
  * Workspace: dsv4_kv4_attention_workspace_size() bytes (of the sizes alone: q, out and lse may be
- * NULL there), 256-byte aligned; what it holds does not matter before the call or after it.
+ * NULL there), 256-byte aligned; what it holds does not matter before the call or after it. A larger
+ * call may need less than a smaller one: where one workspace serves calls of several sizes, take
+ * dsv4_kv4_attention_workspace_limit() of the largest, which is enough for every call with the same
+ * heads and dim whose batch, total_tokens, max_new and cache.max_blocks are no larger (at 128 channels
+ * 5 MB where no sequence brings more than 8 rows, new tokens x query heads of a key/value head; 118 MB
+ * where many do).
  */
 typedef struct {
   int32_t batch;
@@ -579,6 +584,7 @@ typedef struct {
 dsv4_status dsv4_kv4_attention_plan(const dsv4_kv4_attention_args *args, dsv4_kv4_plan *plan);
 
 size_t dsv4_kv4_attention_workspace_size(const dsv4_kv4_attention_args *args);
+size_t dsv4_kv4_attention_workspace_limit(const dsv4_kv4_attention_args *args);
 dsv4_status dsv4_kv4_attention(const dsv4_kv4_attention_args *args, void *workspace, size_t workspace_bytes,
                                dsv4_stream stream);
 

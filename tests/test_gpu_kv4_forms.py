@@ -152,3 +152,25 @@ def test_one_batch_in_every_form():
         out, lse = dsv4.kv4_attention(q, cu, start, x, max_new=max_new, with_lse=True)
         check_attention(x, q, lens, starts, out, lse)
     assert {(A.KV4_STEP, 8), (A.KV4_STEP, 16), (A.KV4_STEP_TENSOR, 8)} <= seen
+
+
+def test_one_workspace_serves_calls_of_all_sizes():
+    """Sized once for the largest, it is enough for smaller calls that split more, and gives the bits that a call's own does."""
+    require_gpu()
+    rng = np.random.default_rng(54)
+    lens, starts = [700, 4, 1], [2000, 600, 9000]
+    c = make_cache(rng, lens, starts, 2, 128, extra_blocks=20)
+    fill_cache(rng, c, lens, starts)
+    q, _ = rand_rows(rng, sum(lens), 8, 128, torch.bfloat16)
+    ws = dsv4.kv4_attention_workspace(q, cu_of(lens), c, max_new=700, smaller=True)
+    one = lambda s: dsv4.DeviceKv4Cache(c.k_codes, c.v_codes, c.k_scales, c.v_scales, c.block_table[s:s + 1])
+    at = np.concatenate([[0], np.cumsum(lens)])
+    forms = set()
+    for s, n in ((0, 700), (0, 40), (1, 4), (2, 1)):
+        a, cu, start = q[at[s]:at[s] + n], cu_of([n]), i32([starts[s]])
+        forms.add(plan_of(a, cu, start, one(s), n).form)
+        want = dsv4.kv4_attention(a, cu, start, one(s), max_new=n, with_lse=True)
+        got = dsv4.kv4_attention(a, cu, start, one(s), max_new=n, with_lse=True, workspace=ws)
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    assert forms == {A.KV4_STEP, A.KV4_PROMPT}
+    dsv4.kv4_attention(q, cu_of(lens), i32(starts), c, max_new=700, workspace=ws)

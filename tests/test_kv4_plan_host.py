@@ -2,6 +2,7 @@
 
 import ctypes as C
 import os
+import random
 import subprocess
 
 import pytest
@@ -61,3 +62,36 @@ def test_plans():
     assert plan(Hq=4, Hk=1, T=300, max_new=300, blocks=64) == (A.KV4_PROMPT, 256, 5, 5, 29)  # few blocks: all are
     # a hint above the tokens there are is the tokens there are
     assert plan(B=4, T=4, max_new=4000, blocks=8) == plan(B=4, T=4, max_new=4, blocks=8)
+
+
+# ---------------------------------------------------------------- the workspace
+
+def test_one_workspace_holds_for_all_smaller_calls(lib):
+    """A call may need more than a larger one (a prompt of 2048 tokens 57 MB, eight of 4096 none); the limit of the largest
+    covers every call below it."""
+    size = lambda a: lib.dsv4_kv4_attention_workspace_size(C.byref(a))
+    limit = lambda a: lib.dsv4_kv4_attention_workspace_limit(C.byref(a))
+    large, one = args(Hq=32, B=8, T=8 * 4096, max_new=4096, blocks=64), args(Hq=32, T=2048, max_new=2048, blocks=64)
+    assert size(large) < size(one) <= limit(large)
+    assert lib.dsv4_kv4_attention_workspace_limit(None) == 0 and limit(args(D=96)) == 0 and limit(args(max_new=0)) == 0
+    rng = random.Random(7)
+    for _ in range(4000):
+        D, Hk, G = rng.choice([64, 128]), rng.choice([1, 2, 3, 4, 6, 8, 16, 20]), rng.choice([1, 2, 4, 5, 8, 16])
+        B, new, blocks = rng.randint(1, 64), int(2 ** rng.uniform(0, 13)), int(2 ** rng.uniform(0, 11))
+        T = rng.randint(new, B * new)
+        top = args(D=D, Hq=Hk * G, Hk=Hk, B=B, T=T, max_new=new, blocks=blocks)
+        most = limit(top)
+        assert size(top) <= most
+        for _ in range(8):
+            b, m, w = rng.randint(1, B), rng.randint(1, new), rng.randint(1, blocks)
+            t = rng.randint(1, min(T, b * m))
+            below = args(D=D, Hq=Hk * G, Hk=Hk, B=b, T=t, max_new=m, blocks=w)
+            assert size(below) <= most and limit(below) <= most, (D, Hk, G, (B, T, new, blocks), (b, t, m, w))
+    # all that any call at all may need
+    assert limit(args(B=4096, T=1 << 26, max_new=1 << 26, blocks=1 << 22)) < 120e6
+
+
+def test_the_limit_is_not_far_above_what_some_call_needs(lib):
+    need = max(lib.dsv4_kv4_attention_workspace_size(C.byref(args(Hq=4 * Hk, Hk=Hk, T=t, max_new=t, blocks=128)))
+               for Hk in (1, 2, 4, 8) for t in range(64, 8192, 64))
+    assert need <= lib.dsv4_kv4_attention_workspace_limit(C.byref(args(Hq=32, T=8192, max_new=8192, blocks=128))) < 1.1 * need
