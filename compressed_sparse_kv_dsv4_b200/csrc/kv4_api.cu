@@ -20,8 +20,10 @@ bool valid_batch(int batch, int total, const int32_t *cu, const int32_t *start) 
   return batch > 0 && batch <= 65535 && total >= 0 && total <= kMaxTokens && cu && start;
 }
 
+// (a base below 1 turns later pairs faster: 2^-16 keeps every angle, at positions below 2^32, within what cos_sin of
+// kv4_heads.cu reduces)
 bool valid_rope(const dsv4_rope &r, int dim) {
-  return r.rope_dims >= 0 && r.rope_dims % 2 == 0 && r.rope_dims <= dim && (r.rope_dims == 0 || r.rope_base > 0.f);
+  return r.rope_dims >= 0 && r.rope_dims % 2 == 0 && r.rope_dims <= dim && (r.rope_dims == 0 || r.rope_base >= 1.52587890625e-5f);
 }
 
 bool valid_kv4(const dsv4_kv4_cache &c) {

@@ -146,7 +146,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-// Sine and cosine of `a` (finite, |a| below 2^31), to about 1e-13 absolute beside the angle's own rounding, rounded once to
+// Sine and cosine of `a` (|a| below 2^48: the entry points see to it), to about 1e-13 absolute beside the angle's own rounding, rounded once to
 // float32: the nearest multiple k of pi/2 is taken off with two constants (pi/2 to 107 bits), the rest, within pi/4, goes
 // into the Taylor polynomials up to r^13 and r^14 (next terms 2e-14 and 1e-15), and k's low bits turn the quadrant.
 // (The library's float64 sincos, which also reduces angles beyond that range, took a one-token call from 4.2 to 4.4 us.)

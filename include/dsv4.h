@@ -434,7 +434,7 @@ dsv4_status dsv4_hybrid_decode(const dsv4_layer *layer, const dsv4_step *step, v
  * tokens at or behind cu_seqlens[batch] are left as they are. Rows of a token's heads are
  * contiguous; tokens are `stride` elements apart (0: heads * dim; otherwise at least that and a
  * multiple of 16 bytes). Row pointers are 16-byte aligned. total_tokens <= 2^26, head counts <=
- * 2^14, batch <= 65535.
+ * 2^14, batch <= 65535. rope_base is at least 2^-16 (any base of a model's is above 1).
  */
 typedef struct {
   void *k_codes, *v_codes;

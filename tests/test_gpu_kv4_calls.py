@@ -263,3 +263,28 @@ def test_small_channels_under_masks_and_missing_pages(Hq, lens, starts, fill):
                 assert np.all(np.abs(got - want[0]) <= limit[0])
                 assert np.all(np.abs(gl - wl[0]) <= (eps + 4 * U * np.abs(wl) + 2.0 ** -21)[0])
             at += n
+
+
+# ---------------------------------------------------------------- angles of far positions
+
+@pytest.mark.parametrize("base", [2.0 ** -16, 0.01, 10000.0])
+def test_rotation_at_the_last_positions(base):
+    """Positions up to 2^31 + 4, and a base that makes their angles 2^47, where only the pair's length is left to check.
+
+    In half steps of float64, 2^-53 relative: theta_1 comes from a pow (2, a whole step); each squaring doubles what there is and adds 1, so
+    theta_1^(2^k) is off by 3 2^k, and the products of those that make up theta_1^i by 3 i and 5 of their own; the position adds 1, the
+    oracle's pow and product 3: 3 i + 9 of the angle, and so much of |a| + |b| of both members of pair i."""
+    require_gpu()
+    rng = np.random.default_rng(61)
+    D, n = 64, 6
+    starts = [2 ** 31 - 1, 2 ** 30 + 12345, 77]
+    lens = [n] * 3
+    q, qv = rand_rows(rng, 3 * n, 2, D, torch.float32)
+    out, _ = dsv4.qk_norm_rope(q, None, cu_of(lens), i32(starts), rope_dims=D, rope_base=base)
+    pos = positions(lens, starts)
+    want = K.norm_rotate(qv, None, 0.0, pos, D, float(np.float32(base)))
+    angle = pos[:, None] * float(np.float32(base)) ** (-2.0 * np.arange(D // 2) / D)
+    eps = 24 * U + np.repeat((3 * np.arange(D // 2) + 9) * 2.0 ** -53 * angle, 2, -1)[:, None]
+    limit = pair_bound(want, D, 1.0) * eps
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= limit + 1e-30)
+    assert np.allclose(np.hypot(out.cpu().numpy()[..., ::2], out.cpu().numpy()[..., 1::2]), np.hypot(qv[..., ::2], qv[..., 1::2]), rtol=1e-6)

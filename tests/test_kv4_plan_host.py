@@ -95,3 +95,17 @@ def test_the_limit_is_not_far_above_what_some_call_needs(lib):
     need = max(lib.dsv4_kv4_attention_workspace_size(C.byref(args(Hq=4 * Hk, Hk=Hk, T=t, max_new=t, blocks=128)))
                for Hk in (1, 2, 4, 8) for t in range(64, 8192, 64))
     assert need <= lib.dsv4_kv4_attention_workspace_limit(C.byref(args(Hq=32, T=8192, max_new=8192, blocks=128))) < 1.1 * need
+
+
+# ---------------------------------------------------------------- the rotation's base
+
+def test_a_base_whose_angles_cannot_be_reduced_is_refused(lib):
+    """Below 2^-16 a pair's angle leaves what the sine and cosine reduce (they would come out of any size)."""
+    from tests.test_kv4_host import _append, _norm
+    nan, inf = float("nan"), float("inf")
+    for base, ok in ((2.0 ** -17, False), (1e-30, False), (nan, False), (-1e4, False), (2.0 ** -16, True), (0.5, True), (inf, True)):
+        for a, call in ((_norm(total_tokens=0), lib.dsv4_qk_norm_rope), (_append(total_tokens=0), lib.dsv4_kv4_append)):
+            a.rope = A.Rope(64, base)
+            assert call(C.byref(a), None) == (A.OK if ok else A.ERR_INVALID_ARG), base
+            a.rope = A.Rope(0, base)  # nothing is turned
+            assert call(C.byref(a), None) == A.OK
