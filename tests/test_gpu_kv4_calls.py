@@ -12,7 +12,7 @@ import oracle.kv4_oracle as K
 import perf.operators as operators
 import synthetic as W
 from tests.parity import require_gpu
-from tests.test_gpu_kv4 import (BF16, U, cache_rows, cu_of, dev, fill_cache, i32, make_cache, pair_bound, positions,
+from tests.test_gpu_kv4 import (BF16, NORM, U, cache_rows, cu_of, dev, fill_cache, i32, make_cache, pair_bound, positions,
                                 rand_rows)
 
 pytestmark = pytest.mark.gpu
@@ -288,3 +288,27 @@ def test_rotation_at_the_last_positions(base):
     limit = pair_bound(want, D, 1.0) * eps
     assert np.all(np.abs(out.double().cpu().numpy() - want) <= limit + 1e-30)
     assert np.allclose(np.hypot(out.cpu().numpy()[..., ::2], out.cpu().numpy()[..., 1::2]), np.hypot(qv[..., ::2], qv[..., 1::2]), rtol=1e-6)
+
+
+# ---------------------------------------------------------------- the norm's bound, for the kernel's own order of sums
+
+@pytest.mark.parametrize("case", NORM, ids=lambda c: f"D{c[0]}-{c[1]}and{c[2]}-{c[6]}-{len(c[3])}")
+def test_norm_rope_within_its_own_roundings(case):
+    """float32 outputs, in units of u = 2^-24. Squares are rounded (1) and summed at a depth of 6 (64 channels) to 10 (512), the mean
+    is exact, eps adds 1: 12, halved by the root, and rsqrtf's two steps 4: 10. The products with it and with gamma: 12 on each
+    channel. Sine and cosine are float64, rounded once (1), of an angle whose float64 error is below 1 at these positions (2^20 of it times
+    9 2^-53 for the fast pairs); product 1 and sum 1: 16 (|a| + |b|) on each of a pair. Without gamma nothing but the rotation: 4, and 0."""
+    require_gpu()
+    D, Hq, Hk, lens, starts, rope, din, _, extra = case
+    rng = np.random.default_rng(D + Hq + 1)
+    T = sum(lens)
+    q, qv = rand_rows(rng, T, max(Hq, 1), D, {"f32": torch.float32, "bf16": torch.bfloat16}[din], extra)
+    g = 1 + 0.3 * rng.standard_normal(D).astype(np.float32)
+    for gamma, turned, kept in ((g, 16, 12), (None, 4, 0)):
+        got, _ = dsv4.qk_norm_rope(q, None, cu_of(lens), i32(starts), gamma_q=None if gamma is None else dev(gamma),
+                                   rope_dims=rope, out_dtype=torch.float32)
+        want = K.norm_rotate(qv, gamma, 1e-6, positions(lens, starts), rope, 10000.0)
+        limit = pair_bound(want, rope, turned * U)
+        limit[..., :D - rope] = kept * U * np.abs(want[..., :D - rope])
+        err = np.abs(got.double().cpu().numpy() - want)
+        assert np.all(err <= limit + 1e-30), (err / (limit + 1e-30)).max()
