@@ -12,7 +12,7 @@
 // parts of the others go through the workspace and kv4_combine_kernel joins them (a fixed
 // order, so results do not depend on timing; where the line is cut depends on the batch).
 //
-// Inside a CTA each of four warps takes every fourth tile whole: it brings its tiles into two or three
+// Inside a CTA each of four warps takes every fourth tile whole: it brings its tiles into two to four
 // stages of its own, half a tile each, with bulk copies (codes and scales of a head's rows are contiguous within a page), and
 // does the products, an online softmax of its own and the weighted sum of values in registers; the
 // warps' sums are joined at the end of the slice's part of the unit. With no producer between them the warps
@@ -20,7 +20,7 @@
 // instructions, some 1340 a tile of 16384 values at 128 channels (conversions, products with the scales,
 // 64 matrix products): 263 us for four sequences of 262144 positions (1.14 GB, 66% of the measured copy rate), 195 us
 // with the arithmetic left out. (The form further down, whose scores are made on the tensor cores, takes long contexts
-// of up to eight rows at 128 channels: 225 us.)
+// of up to eight rows at 128 channels: 233 us.)
 // The matrix products are mma.sync m16n8k16 (fp16 operands, fp32 sums) with
 // keys (S^T = K Q^T) and channels (O^T = V^T P^T) on the 16-row side and rows on the 8-column
 // side: a decode step has G rows, far fewer than a tcgen05 tile's 128, and the operand is made in
@@ -236,7 +236,6 @@ constexpr int resident_ctas(int D, int NT) { return NT == 1 ? 4 : (D == 64 ? 3 :
 template <int D, int NT>
 struct StepShape {
   static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / kKv4Block;
-  static constexpr int kHalf = kCodes + kScales;   // keys or values of a tile
   static constexpr int kStages = D == 64 ? 4 : (NT == 1 ? 2 : 3);  // of a warp, half a tile each
   static constexpr int kResident = resident_ctas(D, NT);
 };
@@ -687,7 +686,8 @@ __global__ void __launch_bounds__(kThreadsA, StepShape<D, NT>::kResident)
 // memory, from where it is the B operand of mma.sync with the values as in the kernel above.
 // The reference of the weights is an integer (so that taking it off twice rounds alike), raised when a score exceeds
 // it by more than 2^8; weights are held times 2^7.
-// Measured: four sequences of 262144 positions 225 us (5.07 TB/s, 77% of the measured copy rate); 194 us with the
+// Measured: four sequences of 262144 positions 233 us (4.90 TB/s, 75% of the measured copy rate; 225 us without what a
+// row's remainder and the rows without a finite score take); 194 us with the
 // arithmetic left out, 195 us without the values' part of it, no less without the copies of the keys. What is left is
 // that part, on three such warps a scheduler: its conversions some 33 us, the products with the scales 7 us, mma.sync
 // nothing. The values' scales are converted once a warp and shared (each lane for itself: 240 us). Four CTAs an SM at
@@ -1288,9 +1288,14 @@ __global__ void __launch_bounds__(kCombineThreads, 8) kv4_combine_kernel(const _
 // Whether the tensor-core form for 256-row blocks takes the call. What it costs goes by blocks of 256 rows in waves
 // over the SMs, however few of their rows there are (1.66 us per 128 keys at 128 channels, 1.54 us at 64); the
 // step form's cost by tiles of 16 rows over the whole card (2.9 ns per 64 keys, 1.9 ns): they meet where
-// there are 283 (409) row tiles to a wave. Measured beside that, at 8 key heads, of 4 query heads each, step form and
-// the other: 8 sequences of 32768 positions, 16 new tokens (256 row tiles) 384 us and 433 us, 32 (512) 747 us
-// and 437 us. Short contexts are latency: 24 us against 15 us for 16 rows and more at 512 positions.
+// there are 283 (409) row tiles to a wave. Where the blocks' keys are split over CTAs a wave's tiles are that much
+// shorter, so the tiles are counted as often. Measured beside that, at 8 key heads of 4 query heads each, step form and the other:
+// 8 sequences of 32768 positions, 16 new tokens (256 row tiles, two splits) 392 us and 236 us, 32 (512) 764 us and
+// 238 us; at 64 channels 246 us and 205 us, 476 us and 207 us. Short contexts, under a table of up to four pages, are
+// latency: 8 sequences of 512 positions, 64 rows each 28.6 us and 14.2 us; one of 16 rows 11.6 us and 13.4 us, but 21 us
+// and 18 us with the host's launches, of which this form makes one.
+// One rule serves all sequences of a call: steps beside a prompt take blocks of 256 rows too (31 steps at 32768 positions and a
+// piece of 2048 tokens of another, 64 query heads: 2855 us, as two calls 1926 us).
 bool prompt_rows(const Kv4AttnLaunch &p, const Kv4PromptShape &g) {
   const int64_t group = p.Hq / p.Hk, rows = (p.max_new < p.T ? p.max_new : p.T) * group;
   if (rows <= 8) return false;
@@ -1330,7 +1335,8 @@ cudaError_t launch_step(AttnParams &P, cudaStream_t st) {
 // longest context that the table holds; with fewer its start and its longer turns show. At 8 key heads of 8 query
 // heads each, the kernel above and this one: 8 sequences of 2000 positions (1024 tiles) 15.7 us and 20.0 us, one of
 // 32000 (2000) 21.4 us and 24.7 us; 64 of 500 (2048) 33.9 us and 26.8 us, 8 of 8000 (4096) 31.8 us and 28.8 us, 8 of
-// 32000 81.4 us and 70.4 us.
+// 32000 81.4 us and 70.4 us. All under tables as wide as the contexts: under a wider one the short ones take this form too (8 of 2000 under
+// 512 pages 21.4 us).
 // Its tensor map wants the codes at a multiple of 32 bytes and rows that an int counts.
 bool tensor_scores(const Kv4AttnLaunch &p, int rows) {
   return p.D == 128 && rows == 8 && turns_of_8(p) >= int64_t(4) * (kTcKeys / kTile) * kTcResident * sm_count() &&

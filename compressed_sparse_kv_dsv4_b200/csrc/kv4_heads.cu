@@ -17,13 +17,16 @@
 // their way into shared memory (cp.async, each thread its own pieces, so nothing waits for anything but its
 // own data); the angles of a token are worked out once, by one thread per pair and token, and shared by all its heads.
 //
-// Measured: 8 x 4096 tokens of 64 query and 8 key heads of 128 channels in bf16 202 us (1.21 GB, 91% of the measured copy
-// rate), appended with 8 value heads 225 us (1.38 GB, 93%).
+// Measured: 8 x 4096 tokens of 64 query and 8 key heads of 128 channels in bf16 197 us (1.21 GB, 93% of the measured copy
+// rate), appended with 8 value heads 222 us (1.38 GB, 95%), both captured; as calls among others 212 us (87%) and 250 us (84%).
+// As many bytes of 256 or 512 channels 225 us, in float32 280 us at 128 channels and 300 us at 256 and 512 (two turns
+// of rows are on their way there, not three).
 //
-// Rounding to 4 bits makes a whole step out of one bit of float32 next to a border, so the float32
-// part is kept in the textbook's order: squares rounded, then summed (four neighbours in turn at 128
-// channels, channels 32 apart at 64; then halves onto halves), x * (1 / rms) * gamma, products of the
-// rotation rounded before their difference; angle, sine and cosine in float64.
+// Rounding to 4 bits makes a whole step out of one bit of float32 next to a border, so the float32 part keeps the order of the
+// plain float32 program that it is compared with (perf/operators.py), whose row sums go by four neighbours in turn at 128 channels
+// and by channels 32 apart at 64, then halves onto halves: codes next to a border then agree. 256 and 512 channels, which are not
+// rounded to 4 bits, take the order of 128. Squares are rounded, then summed; x * (1 / rms) * gamma; products of the rotation
+// are rounded before their difference; angle, sine and cosine in float64.
 #include <type_traits>
 
 #include "kv4_device.cuh"

@@ -16,8 +16,8 @@
 // Softmax: the reference R that weights are taken against is raised (and O scaled) only when a
 // tile's maximum exceeds it by more than 2^8; weights are held times 2^7, at most 2^15 in fp16.
 // With few blocks of rows the keys of a block are split over CTAs, which a second kernel joins.
-// Measured: eight prompts of 4096 tokens, 32 heads over 8 of 128 channels, 1150 us (956 TFLOP/s); 2048 tokens behind
-// 14336 442 us (1165 TFLOP/s; 457 us without the last wave shared out); a tile pair of 256 x 128 takes 1.85 us, 1342 TFLOP/s.
+// Measured: eight prompts of 4096 tokens, 32 heads over 8 of 128 channels, 1155 us (952 TFLOP/s); 2048 tokens behind
+// 14336 442 us (1167 TFLOP/s; 457 us without the last wave shared out); a tile pair of 256 x 128 takes 1.85 us, 1342 TFLOP/s.
 // A thread keeps its S row in 128 registers between the maximum and the weights (the warpgroups'
 // registers are split 184, 184, 96, 48), and hands its weights over in halves of 64 keys.
 #include "kv4_device.cuh"

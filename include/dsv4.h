@@ -435,6 +435,10 @@ dsv4_status dsv4_hybrid_decode(const dsv4_layer *layer, const dsv4_step *step, v
  * contiguous; tokens are `stride` elements apart (0: heads * dim; otherwise at least that and a
  * multiple of 16 bytes). Row pointers are 16-byte aligned. total_tokens <= 2^26, head counts <=
  * 2^14, batch <= 65535. rope_base is at least 2^-16 (any base of a model's is above 1).
+ *
+ * The rotation is the library's: the last rope_dims channels, adjacent pairs (2i, 2i + 1). For a model
+ * that rotates the halves of those channels against each other, or its first channels, permute the
+ * channels of its query and key projections (and gamma) once: scores do not depend on their order.
  */
 typedef struct {
   void *k_codes, *v_codes;
@@ -531,8 +535,10 @@ dsv4_status dsv4_kv4_append(const dsv4_kv4_append_args *args, dsv4_stream stream
  *   q, out [total_tokens][heads][dim] bf16 (q strided, out dense), dim 64 or 128, q as
  *   dsv4_kv4_append leaves it; lse [total_tokens][heads] float32 or NULL; softmax_scale <= 0
  *   means 1/sqrt(dim).
- *   max_new: the most new tokens that a sequence of the batch brings. It chooses the kernel;
- *   results are right for any value >= 1.
+ *   max_new: the most new tokens that a sequence of the batch brings. It chooses the kernel (see
+ *   dsv4_kv4_attention_plan); results are right for any value >= 1. One kernel takes the whole call:
+ *   steps beside a prompt are faster as a call of their own, and a table that is much wider than the
+ *   contexts may take a short step to the kernel for long ones.
  * Positions on a page with an id out of range are left out and reported; positions beyond the
  * table's capacity do not exist (reported). A row that is left with no position gets a zero output
  * and lse -inf. A NaN in a key or value makes NaN of the rows that see it and of no other. A query
