@@ -573,7 +573,7 @@ typedef struct {
 /*
  * dsv4_kv4_attention_plan: how a call with these arguments is carried out, without making it (host
  * only; q, out and lse may be NULL). It follows from max_new, total_tokens, batch, the heads, dim, the
- * table's width (the longest context that it holds) and the alignment of k_codes.
+ * table's width (the longest context that it holds), num_pages and the alignment of k_codes.
  *   DSV4_KV4_STEP         tiles of 8 or 16 rows (new tokens x query heads of a key/value head)
  *   DSV4_KV4_STEP_TENSOR  tiles of 8 rows, scores on the tensor cores: dim 128, wide tables
  *   DSV4_KV4_PROMPT       blocks of 256 rows; `units` blocks of all sequences and key/value heads, the keys of
