@@ -743,7 +743,7 @@ __device__ __forceinline__ void tc_missing(const Kv4AttnLaunch &p, const TcStepS
     uint32_t h[4];
     e2m1x8_to_half2(codes[c], h);
     const uint32_t byte = scales >> (c / 4 * 8) & 255u;
-    const float f = byte > 127u + kKv4ExpMax ? 0.f : __uint_as_float(byte << 23);  // (a NaN block, or behind the last position)
+    const float f = byte > 127u + kKv4ExpMax ? 0.f : __uint_as_float(byte << 23);  // (a NaN block)
     float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -945,7 +945,6 @@ __device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Wa
     }
     // 2^(byte - 127) * missing is above kTcLoose where the byte is above 104 + 127 - wide: the sum of a scale byte (104 to
     // 140) less 104 and `wide` then has its upper bit. Four bytes at once.
-    // (Bytes behind the last position may be anything, and then it may too: what is added there is masked.)
     float missing = 0.f;
 #pragma unroll
     for (int r = 0; r < R; ++r) missing = fmaxf(missing, S.missing[r]);
@@ -972,10 +971,10 @@ __device__ __forceinline__ void tc_attend(const AttnParams &P, TcStepSmem &S, Wa
         const bool bad = S.bad[slot];
         const int key0 = (w.tile + i) * kTcKeys + 32 * warp;  // the warp's first key
         const bool edge = key0 + 32 > least;
-        const uint32_t kb = *reinterpret_cast<const uint32_t *>(T.ks + 4 * (32 * warp + lane));
-        if (!decltype(exact)::value && __any_sync(0xFFFFFFFFu, (kb + wide4) & 0x80808080u)) break;
+        uint32_t kb = *reinterpret_cast<const uint32_t *>(T.ks + 4 * (32 * warp + lane));
         uint32_t vb = *reinterpret_cast<const uint32_t *>(T.vs + 4 * (32 * warp + lane));
-        if ((edge || bad) && (bad || key0 + lane >= limit)) vb = 0;  // not a position of the unit
+        if ((edge || bad) && (bad || key0 + lane >= limit)) kb = 0x68686868u, vb = 0;  // not a position of the unit
+        if (!decltype(exact)::value && __any_sync(0xFFFFFFFFu, (kb + wide4) & 0x80808080u)) break;
         if (vb & vb << 1 & 0x80808080u) {  // no scale but NaN's byte has its two upper bits
 #pragma unroll
           for (int b = 0; b < 4; ++b)
@@ -1333,9 +1332,9 @@ cudaError_t launch_step(AttnParams &P, cudaStream_t st) {
 
 // The form with scores on the tensor cores takes calls of at least four of its tiles for each of its CTAs, going by the
 // longest context that the table holds; with fewer its start and its longer turns show. At 8 key heads of 8 query
-// heads each, the kernel above and this one: 8 sequences of 2000 positions (1024 tiles) 15.7 us and 20.0 us, one of
-// 32000 (2000) 21.4 us and 24.7 us; 64 of 500 (2048) 33.9 us and 26.8 us, 8 of 8000 (4096) 31.8 us and 28.8 us, 8 of
-// 32000 81.4 us and 70.4 us. All under tables as wide as the contexts: under a wider one the short ones take this form too (8 of 2000 under
+// heads each, the kernel above and this one: 8 sequences of 2000 positions (1024 tiles) 16.1 us and 21.4 us, one of
+// 32000 (2000) 22.1 us and 26.0 us; 64 of 500 (2048) 30.1 us and 29.0 us, 8 of 8000 (4096) 32.0 us and 30.3 us, 8 of
+// 32000 81.3 us and 73.0 us. All under tables as wide as the contexts: under a wider one the short ones take this form too (8 of 2000 under
 // 512 pages 21.4 us).
 // Its tensor map wants the codes at a multiple of 32 bytes and rows that an int counts.
 bool tensor_scores(const Kv4AttnLaunch &p, int rows) {
