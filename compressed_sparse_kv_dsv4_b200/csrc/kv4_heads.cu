@@ -253,8 +253,14 @@ __global__ void __launch_bounds__(kHThreads, 3) kv4_heads_kernel(const __grid_co
             for (int i = 8 * c; i < 8 * c + 8; i += 4) {
               const ulonglong2 v = cs[(i & 4) / 4];
               const uint64_t a = pack_f32x2(x[i], x[i + 2]), b = pack_f32x2(x[i + 1], x[i + 3]);
-              unpack_f32x2(sub_f32x2(mul_f32x2(a, v.x), mul_f32x2(b, v.y)), x[i], x[i + 2]);
-              unpack_f32x2(add_f32x2(mul_f32x2(a, v.y), mul_f32x2(b, v.x)), x[i + 1], x[i + 3]);
+              // (sums one by one: a packed sum of packed products is made one operation, .rn or not)
+              float p0, p1, q0, q1, r0, r1, s0, s1;
+              unpack_f32x2(mul_f32x2(a, v.x), p0, p1);
+              unpack_f32x2(mul_f32x2(b, v.y), q0, q1);
+              unpack_f32x2(mul_f32x2(a, v.y), r0, r1);
+              unpack_f32x2(mul_f32x2(b, v.x), s0, s1);
+              x[i] = __fsub_rn(p0, q0), x[i + 2] = __fsub_rn(p1, q1);
+              x[i + 1] = __fadd_rn(r0, s0), x[i + 3] = __fadd_rn(r1, s1);
             }
           }
         } else {

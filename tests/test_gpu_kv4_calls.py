@@ -312,3 +312,29 @@ def test_norm_rope_within_its_own_roundings(case):
         limit[..., :D - rope] = kept * U * np.abs(want[..., :D - rope])
         err = np.abs(got.double().cpu().numpy() - want)
         assert np.all(err <= limit + 1e-30), (err / (limit + 1e-30)).max()
+
+
+@pytest.mark.parametrize("D,rope", [(64, 64), (128, 64), (128, 20), (512, 64)])
+@pytest.mark.parametrize("norm", [False, True])
+def test_rotation_rounds_each_product(D, rope, norm):
+    """The float32 steps are those of a plain float32 program, so that a key next to a border of its 4-bit codes gets the same
+    code: the outputs agree to the last bit, but where a sine or cosine lies within its angle's float64 error (12 2^-53 of 4096 turns at the
+    most, 5e-12) of a border between float32 values (6e-8 apart): one in ten thousand. Products contracted into their sums differ
+    in a quarter of the rotated channels."""
+    require_gpu()
+    x = torch.randn((4096, 4, D), device="cuda", generator=torch.Generator("cuda").manual_seed(D + rope))
+    g = (1 + 0.2 * torch.randn(D, device="cuda", generator=torch.Generator("cuda").manual_seed(1))) if norm else None
+    got, _ = dsv4.qk_norm_rope(x, None, cu_of([4096]), i32([0]), gamma_q=g, rope_dims=rope, eps=operators.EPS)
+    pos = torch.arange(4096, device="cuda")
+    want = x
+    if norm and D <= 128:  # (the plain program's row sums are those of 64 and 128 channels)
+        want = operators._norm_rotate(x, g, pos, 0, 1e4)
+    elif norm:
+        want, _ = dsv4.qk_norm_rope(x, None, cu_of([4096]), i32([0]), gamma_q=g, rope_dims=0, eps=operators.EPS)
+    theta = 1e4 ** (-2.0 / rope * torch.arange(rope // 2, dtype=torch.float64, device="cuda"))
+    angle = pos.double()[:, None, None] * theta
+    c, s = torch.cos(angle).float(), torch.sin(angle).float()
+    a, b = want[..., D - rope::2], want[..., D - rope + 1::2]
+    want = torch.cat([want[..., :D - rope], torch.stack([a * c - b * s, a * s + b * c], -1).flatten(-2)], -1)
+    assert torch.equal(got[..., :D - rope], want[..., :D - rope])
+    assert (got != want).double().mean().item() < 1e-3
