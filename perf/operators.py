@@ -251,9 +251,9 @@ def _own(s):
                                  rope_dims=c["rope"], rope_base=BASE)
         return dict(q=q, k=k)
     if c["op"] == "append":
-        more = {}
-        if c["heads"]:  # (the call's own output would be bfloat16 whatever the queries are)
-            more = dict(q=s["q"], gamma_q=s["gamma_q"], q_out=torch.empty(s["q"].shape, dtype=s["q"].dtype, device=s["q"].device))
+        more = dict(q=s["q"], gamma_q=s["gamma_q"]) if c["heads"] else {}
+        if c["heads"] and c["dtype"] != "bf16":  # (the call's own output is bfloat16 whatever the queries are)
+            more["q_out"] = torch.empty(s["q"].shape, dtype=s["q"].dtype, device=s["q"].device)
         q, k, v = dsv4.kv4_append(s["k"], s["v"], s["cu"], s["start"], s["cache"], gamma_k=s["gamma_k"], eps=EPS,
                                   rope_dims=c["rope"], rope_base=BASE, with_stored=True, **more)
         return dict(q=q, k=k, v=v)
